@@ -1,0 +1,416 @@
+// The operators around the products of a routed FFN: the router
+// (prox_expert_route), the quantizer to e4m3 (prox_fp8_quantize) and the
+// weighted sum of a token's expert rows (prox_expert_combine).
+#include <float.h>
+
+#include "experts_internal.h"
+#include "prox_device.h"
+
+namespace prox {
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4_t;
+
+// ------------------------------------------------------------------- router
+// A logit as an unsigned key: larger keys are larger logits, 0 (-inf) is never
+// chosen, NaN comes first and makes the token's weights NaN; +inf counts as the
+// largest finite value, so that the softmax below has no inf - inf.
+__device__ __forceinline__ uint32_t route_key(float z) {
+  if (z != z) return 0xFFFFFFFFu;
+  if (z == -INFINITY) return 0u;
+  const uint32_t b = __float_as_uint(fminf(z, FLT_MAX) + 0.0f);  // -0 orders with +0
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float route_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
+}
+
+constexpr int kRouteThreads = 256;
+constexpr int kRouteSub = 64;      // tokens of one bitmap pass: the bits of a word
+constexpr int kRouteBlocks = 256;  // blocks at most
+
+// Tokens per block: whole passes of kRouteSub beyond kRouteBlocks blocks of 32.
+__host__ __device__ inline int route_tokens_per_block(int tokens) {
+  if (tokens <= 32 * kRouteBlocks) return 32;
+  const int per = (tokens + kRouteBlocks - 1) / kRouteBlocks;
+  return (per + kRouteSub - 1) / kRouteSub * kRouteSub;
+}
+
+// The top_k of one token by one wave: kPer logits a lane, expert lane + 64 i.
+// Each round takes the largest key, the lowest expert among equals.
+template <int kPer>
+__device__ __forceinline__ void route_token(const RouteArgs& a, int token, int lane) {
+  uint32_t key[kPer];
+  const size_t base = static_cast<size_t>(token) * a.experts;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + 64 * i;
+    key[i] = 0;
+    if (e < a.experts)
+      key[i] = route_key(a.logits_dtype == PROX_F32 ? load_elem<F32Tag>(a.logits, base + e)
+                                                    : load_elem<Bf16Tag>(a.logits, base + e));
+  }
+  uint32_t all[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) all[i] = key[i];
+  uint32_t my_key = 0;  // lane s holds slot s
+  int my_id = -1;
+  float top = 0.f;
+  for (int s = 0; s < a.top_k; ++s) {
+    uint32_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+    // (key, lowest expert) as one 64-bit maximum
+    uint64_t v = (static_cast<uint64_t>(best) << 32) | static_cast<uint32_t>(~(lane + 64 * at));
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const uint64_t o = __shfl_xor(v, m);
+      v = o > v ? o : v;
+    }
+    const uint32_t k = static_cast<uint32_t>(v >> 32);
+    if (k == 0) break;  // uniform: no expert is left
+    const int e = static_cast<int>(~static_cast<uint32_t>(v));
+    if (s == 0) top = route_value(k);
+    if (lane == s) {
+      my_key = k;
+      my_id = e;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 64 * i == e) key[i] = 0;
+  }
+  const float p = my_id >= 0 ? expf(route_value(my_key) - top) : 0.f;
+  float part = p;
+  if (!a.renormalize) {
+    part = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (all[i] != 0) part += expf(route_value(all[i]) - top);
+  }
+  const float total = wave_sum(part);
+  if (lane < a.top_k) {
+    const size_t o = static_cast<size_t>(token) * a.top_k + lane;
+    a.expert_idx[o] = my_id;
+    a.weight[o] = my_id >= 0 ? p / total : 0.f;
+  }
+}
+
+// The chosen experts of up to kRouteSub tokens from t0 on as one bitmap word
+// per expert (bit = token): a token takes an expert at most once, so the place
+// of (token, expert) among the tokens is a population count.
+__device__ __forceinline__ void route_bitmap(const RouteArgs& a, int t0, int nt, unsigned long long* bits) {
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) bits[e] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * a.top_k; i += kRouteThreads) {
+    const int t = i / a.top_k;
+    const int e = a.expert_idx[static_cast<size_t>(t0) * a.top_k + i];
+    if (e >= 0) atomicOr(&bits[e], 1ull << t);
+  }
+  __syncthreads();
+}
+
+// First launch: experts and weights of the block's tokens, and how many rows
+// each expert gets from them.
+template <int kPer>
+__global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(RouteArgs a) {
+  __shared__ int count[kMaxExperts];
+  const int per = route_tokens_per_block(a.tokens);
+  const int t0 = blockIdx.x * per, t1 = min(a.tokens, t0 + per);
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
+  const int lane = threadIdx.x & 63;
+  for (int t = t0 + (threadIdx.x >> 6); t < t1; t += kRouteThreads / 64) route_token<kPer>(a, t, lane);
+  __syncthreads();
+  for (int i = threadIdx.x; i < (t1 - t0) * a.top_k; i += kRouteThreads) {
+    const int e = a.expert_idx[static_cast<size_t>(t0) * a.top_k + i];
+    if (e >= 0) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads)
+    a.block_count[static_cast<size_t>(blockIdx.x) * a.experts + e] = count[e];
+}
+
+// Second launch: every block adds up the counts of all blocks (so that no block
+// waits for another), then places its own rows.
+__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(RouteArgs a, int blocks) {
+  __shared__ int next[kMaxExperts];   // the next row of each expert
+  __shared__ int total[kMaxExperts];
+  __shared__ unsigned long long bits[kMaxExperts];
+  __shared__ int wave_total[kRouteThreads / 64];
+  const int tid = threadIdx.x;
+  for (int e = tid; e < a.experts; e += kRouteThreads) {
+    int before = 0, sum = 0;
+    for (int b = 0; b < blocks; ++b) {
+      const int c = a.block_count[static_cast<size_t>(b) * a.experts + e];
+      if (b < static_cast<int>(blockIdx.x)) before += c;
+      sum += c;
+    }
+    next[e] = before;
+    total[e] = sum;
+  }
+  __syncthreads();
+  // exclusive sums over the experts: each thread a run of neighbouring ones
+  const int per = (a.experts + kRouteThreads - 1) / kRouteThreads;
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    if (e < a.experts) mine += total[e];
+  }
+  int start = wave_inclusive_scan_int(mine);
+  if ((tid & 63) == 63) wave_total[tid >> 6] = start;
+  __syncthreads();
+  start -= mine;
+  int rows = 0;
+  for (int w = 0; w < kRouteThreads / 64; ++w) {
+    if (w < (tid >> 6)) start += wave_total[w];
+    rows += wave_total[w];
+  }
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    if (e < a.experts) {
+      if (blockIdx.x == 0) a.offsets[e] = start;
+      next[e] += start;
+      start += total[e];
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = rows;
+  const int tpb = route_tokens_per_block(a.tokens);
+  const int t0 = blockIdx.x * tpb, t1 = min(a.tokens, t0 + tpb);
+  for (int s0 = t0; s0 < t1; s0 += kRouteSub) {
+    const int nt = min(kRouteSub, t1 - s0);
+    route_bitmap(a, s0, nt, bits);  // its first barrier also covers next[]
+    for (int i = tid; i < nt * a.top_k; i += kRouteThreads) {
+      const int t = i / a.top_k;
+      const size_t o = static_cast<size_t>(s0) * a.top_k + i;
+      const int e = a.expert_idx[o];
+      int row = -1;
+      if (e >= 0) {
+        row = next[e] + __popcll(bits[e] & ((1ull << t) - 1));
+        a.row_token[row] = s0 + t;
+      }
+      a.row_of[o] = row;
+    }
+    __syncthreads();
+    for (int e = tid; e < a.experts; e += kRouteThreads) next[e] += __popcll(bits[e]);
+    __syncthreads();
+  }
+  // rows behind the last expert's
+  const int all = a.tokens * a.top_k;
+  for (int r = rows + blockIdx.x * kRouteThreads + tid; r < all; r += blocks * kRouteThreads) a.row_token[r] = -1;
+}
+
+// ---------------------------------------------------------------- quantizer
+// 8 neighbouring values as fp32
+template <typename T> __device__ __forceinline__ void load8(const uint8_t* p, float v[8]);
+template <> __device__ __forceinline__ void load8<Bf16Tag>(const uint8_t* p, float v[8]) {
+  const u32x4_t w = *reinterpret_cast<const u32x4_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16lo(w[i]);
+    v[2 * i + 1] = bf16hi(w[i]);
+  }
+}
+template <> __device__ __forceinline__ void load8<F32Tag>(const uint8_t* p, float v[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x4_t w = reinterpret_cast<const f32x4_t*>(p)[h];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * h + i] = w[i];
+  }
+}
+
+// The largest |v| as bits: integer order puts finite values below infinity and
+// infinity below NaN, so a block with either is seen.
+__device__ __forceinline__ uint32_t abs_bits8(const float v[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+// The scale fp32(amax / 448); NaN where the block holds an infinity or NaN.
+__device__ __forceinline__ float block_scale(uint32_t amax) {
+  return amax < 0x7F800000u ? __uint_as_float(amax) / 448.0f : __uint_as_float(0x7FC00000u);
+}
+
+// e4m3(fp32(v / scale)) of 8 values.  scale 0 (an all-zero block): zeros.
+__device__ __forceinline__ uint2 to_e4m3(const float v[8], float scale) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = scale == 0.f ? 0.f : v[i] / scale;
+  if (scale != scale) return uint2{0x7F7F7F7Fu, 0x7F7F7F7Fu};
+  uint2 r;
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
+  r.x = static_cast<uint32_t>(lo);
+  r.y = static_cast<uint32_t>(hi);
+  return r;
+}
+
+// Rows: sixteen lanes hold the 128 values of a block.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeArgs a) {
+  const int kblocks = (a.k + kScaleBlock - 1) / kScaleBlock;
+  const int64_t block = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
+  if (block >= static_cast<int64_t>(a.rows) * kblocks) return;
+  const int64_t row = block / kblocks;
+  const int col = static_cast<int>(block % kblocks) * kScaleBlock + (threadIdx.x & 15) * 8;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  const bool in = col < a.k;
+  if (in) load8<T>(a.x + row * a.x_stride + static_cast<int64_t>(col) * sizeof(typename T::storage), v);
+  uint32_t m = abs_bits8(v);
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d)));
+  const float scale = block_scale(m);
+  if (in) *reinterpret_cast<uint2*>(a.q + row * a.q_stride + col) = to_e4m3(v, scale);
+  if ((threadIdx.x & 15) == 0) a.scale[block] = scale;
+}
+
+// Square blocks of weights: one workgroup per 128 x 128.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_square_kernel(QuantizeArgs a) {
+  __shared__ uint32_t wave_max[4];
+  const int kblocks = (a.k + kScaleBlock - 1) / kScaleBlock;
+  const int64_t rb = blockIdx.x / kblocks;
+  const int cb = blockIdx.x % kblocks;
+  const int col = cb * kScaleBlock + (threadIdx.x & 15) * 8;
+  float v[8][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = rb * kScaleBlock + i * 16 + (threadIdx.x >> 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    if (row < a.rows && col < a.k)
+      load8<T>(a.x + row * a.x_stride + static_cast<int64_t>(col) * sizeof(typename T::storage), v[i]);
+    m = max(m, abs_bits8(v[i]));
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d)));
+  if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = max(max(wave_max[0], wave_max[1]), max(wave_max[2], wave_max[3]));
+  const float scale = block_scale(m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = rb * kScaleBlock + i * 16 + (threadIdx.x >> 4);
+    if (row < a.rows && col < a.k) *reinterpret_cast<uint2*>(a.q + row * a.q_stride + col) = to_e4m3(v[i], scale);
+  }
+  if (threadIdx.x == 0) a.scale[rb * kblocks + cb] = scale;
+}
+
+// ------------------------------------------------------------------ combine
+// A thread adds up kVec neighbouring values of one token, slot by slot in
+// fp32; the order of the sum is that of the slots, whatever the launch.
+template <typename T, int kOut, int kVec>
+__global__ void __launch_bounds__(256) combine_kernel(CombineArgs a, int blocks_per_token) {
+  const int token = blockIdx.x / blocks_per_token;
+  const int j = ((blockIdx.x % blocks_per_token) * blockDim.x + threadIdx.x) * kVec;
+  if (j >= a.n) return;
+  float acc[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
+  const size_t slot0 = static_cast<size_t>(token) * a.top_k;
+  for (int s = 0; s < a.top_k; ++s) {
+    const int row = a.row_of[slot0 + s];
+    if (row < 0 || row >= a.h_rows) continue;
+    const float w = a.weight[slot0 + s];
+    const uint8_t* p = a.h + row * a.h_stride;
+    float v[kVec];
+    if constexpr (kVec == 8) load8<T>(p + static_cast<int64_t>(j) * sizeof(typename T::storage), v);
+    else v[0] = load_elem<T>(p, j);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+  }
+  uint8_t* q = a.y + token * a.y_stride;
+  if constexpr (kOut == PROX_F32) {
+    float* y = reinterpret_cast<float*>(q) + j;
+    if constexpr (kVec == 8) {
+      reinterpret_cast<f32x4_t*>(y)[0] = f32x4_t{acc[0], acc[1], acc[2], acc[3]};
+      reinterpret_cast<f32x4_t*>(y)[1] = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
+    } else {
+      y[0] = acc[0];
+    }
+  } else {
+    __bf16* y = reinterpret_cast<__bf16*>(q) + j;
+    if constexpr (kVec == 8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        reinterpret_cast<bf16x4_t*>(y)[h] = bf16x4_t{(__bf16)acc[4 * h], (__bf16)acc[4 * h + 1],
+                                                     (__bf16)acc[4 * h + 2], (__bf16)acc[4 * h + 3]};
+    } else {
+      y[0] = (__bf16)acc[0];
+    }
+  }
+}
+
+template <typename T, int kOut, int kVec>
+hipError_t launch_combine_typed(const CombineArgs& a, hipStream_t s) {
+  const int threads = std::min(256, ((a.n + kVec - 1) / kVec + 63) / 64 * 64);
+  const int per = (a.n + kVec * threads - 1) / (kVec * threads);
+  const int64_t grid = static_cast<int64_t>(a.tokens) * per;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  combine_kernel<T, kOut, kVec><<<dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s>>>(a, per);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_combine_type(const CombineArgs& a, hipStream_t s) {
+  if (a.y_dtype == PROX_F32)
+    return a.vec ? launch_combine_typed<T, PROX_F32, 8>(a, s) : launch_combine_typed<T, PROX_F32, 1>(a, s);
+  return a.vec ? launch_combine_typed<T, PROX_BF16, 8>(a, s) : launch_combine_typed<T, PROX_BF16, 1>(a, s);
+}
+
+int route_blocks(int tokens) {
+  const int per = route_tokens_per_block(tokens);
+  return std::max(1, (tokens + per - 1) / per);
+}
+
+}  // namespace
+
+size_t route_workspace(int tokens, int experts, int top_k) {
+  (void)top_k;
+  return (static_cast<size_t>(route_blocks(tokens)) * experts * sizeof(int) + 255) & ~static_cast<size_t>(255);
+}
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+  const int blocks = route_blocks(a.tokens);
+  const dim3 grid(blocks), block(kRouteThreads);
+  if (a.experts <= 64) route_choose_kernel<1><<<grid, block, 0, s>>>(a);
+  else if (a.experts <= 128) route_choose_kernel<2><<<grid, block, 0, s>>>(a);
+  else if (a.experts <= 256) route_choose_kernel<4><<<grid, block, 0, s>>>(a);
+  else route_choose_kernel<16><<<grid, block, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  route_place_kernel<<<grid, block, 0, s>>>(a, blocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s) {
+  const int64_t kblocks = (a.k + kScaleBlock - 1) / kScaleBlock;
+  const int64_t grid = a.block_rows == 1 ? (a.rows * kblocks + 15) / 16
+                                         : (a.rows + kScaleBlock - 1) / kScaleBlock * kblocks;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const dim3 g(static_cast<unsigned>(grid)), b(256);
+  if (a.block_rows == 1) {
+    if (a.x_dtype == PROX_F32) quantize_rows_kernel<F32Tag><<<g, b, 0, s>>>(a);
+    else quantize_rows_kernel<Bf16Tag><<<g, b, 0, s>>>(a);
+  } else {
+    if (a.x_dtype == PROX_F32) quantize_square_kernel<F32Tag><<<g, b, 0, s>>>(a);
+    else quantize_square_kernel<Bf16Tag><<<g, b, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const CombineArgs& a, hipStream_t s) {
+  return a.h_dtype == PROX_F32 ? launch_combine_type<F32Tag>(a, s) : launch_combine_type<Bf16Tag>(a, s);
+}
+
+}  // namespace prox

@@ -10,14 +10,17 @@
 #include <string>
 #include <vector>
 
-#include "prox_internal.h"
+#include "experts_internal.h"
 
 #define PROX_API extern "C" __attribute__((visibility("default")))
 
 namespace prox {
-namespace {
 
+namespace {
 thread_local std::string g_err;
+}
+
+void clear_error() { g_err.clear(); }
 
 prox_status fail(prox_status st, const char* fmt, ...) {
   char buf[512];
@@ -32,6 +35,8 @@ prox_status fail(prox_status st, const char* fmt, ...) {
 prox_status hip_fail(hipError_t e, const char* what) {
   return fail(PROX_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+namespace {
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
@@ -221,10 +226,6 @@ hipError_t for_each_group(int32_t batch, Fn fn) {
   return hipSuccess;
 }
 
-// CUs of the current device (the channel-major Stage-1 grid: one block per
-// CU), cached per device; 256 if the query fails.
-int device_cus();
-
 // Channel-major Stage 1 of one group of nt tokens (ws: the group's first slice).
 QtArgs qt_args(const Plan& p, const prox_layer* L, const void* x, float tau_x, float tau_s, void* ws,
                float* s_tilde, int* in_count, int nt) {
@@ -314,6 +315,9 @@ int fused_grid(int wdtype, size_t smem) {
   return di.cus;
 }
 
+}  // namespace
+
+// CUs of the current device, cached per device; 256 if the query fails.
 int device_cus() {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 256;
@@ -324,6 +328,8 @@ int device_cus() {
     di.cus = 0;
   return di.cus > 0 ? di.cus : 256;
 }
+
+namespace {
 
 // Checks of prox_ffn_decode's arguments other than the workspace.
 prox_status check_decode_args(const prox_layer* layer, const void* x, int32_t batch, float tau_x, float tau_s,

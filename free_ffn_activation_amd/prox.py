@@ -24,6 +24,7 @@ PROX_ERR_HIP = -3
 PROX_ERR_INTERNAL = -4
 PROX_F32 = 0
 PROX_BF16 = 1
+PROX_FP8 = 2  # e4m3, routed-FFN products only
 PROX_ACT_SILU = 0
 PROX_ACT_GELU_TANH = 1
 PROX_PROXY_INT4 = 0
@@ -45,7 +46,8 @@ EXPORTED = ("prox_abi_version", "prox_last_error", "prox_layer_sizes", "prox_wor
             "prox_proxy_qt_size", "prox_pack_proxy_qt",
             "prox_calibrate", "prox_calibrate_hist_workspace_size", "prox_calibrate_hist", "prox_ffn_decode", "prox_ffn_decode_noalloc", "prox_ffn_decode_events",
             "prox_ffn_decode_stages", "prox_ffn_stage2", "prox_proxy_state", "prox_workspace_check",
-            "prox_set_wait_limit")
+            "prox_set_wait_limit", "prox_grouped_matmul", "prox_expert_route_workspace_size", "prox_expert_route",
+            "prox_fp8_quantize", "prox_expert_combine", "prox_moe_workspace_size", "prox_moe_ffn")
 
 
 class ProxError(RuntimeError):
@@ -67,6 +69,20 @@ class prox_layer(ctypes.Structure):
                 ("proxy_q", _c_vp), ("proxy_scale", _c_vp), ("w_upgate_t", _c_vp),
                 ("w_down", _c_vp), ("proxy_kind", _c_i32), ("reserved", _c_i32), ("proxy_w16", _c_vp),
                 ("proxy_qt", _c_vp)]
+
+
+_c_i64 = ctypes.c_int64
+
+
+class prox_experts(ctypes.Structure):
+    _fields_ = [("n_groups", _c_i32), ("n", _c_i32), ("k", _c_i32), ("wdtype", _c_i32), ("activation", _c_i32),
+                ("reserved", _c_i32), ("row_stride", _c_i64), ("group_stride", _c_i64), ("w", _c_vp),
+                ("w_gate", _c_vp), ("w_scale", _c_vp), ("w_gate_scale", _c_vp)]
+
+
+class prox_moe_layer(ctypes.Structure):
+    _fields_ = [("up", prox_experts), ("down", prox_experts), ("w_router", _c_vp), ("top_k", _c_i32),
+                ("renormalize", _c_i32), ("reserved", _c_i32)]
 
 
 _P = ctypes.POINTER
@@ -103,6 +119,16 @@ _sig = {
                                   _c_size, _c_vp]),
     "prox_workspace_check": (_c_i32, [_c_vp, _c_size, _c_vp]),
     "prox_set_wait_limit": (_c_i32, [ctypes.c_uint32, _P(ctypes.c_uint32)]),
+    "prox_grouped_matmul": (_c_i32, [_P(prox_experts), _c_vp, _c_i32, _c_i64, _c_vp, _c_vp, _c_vp, _c_i32, _c_vp,
+                                     _c_i32, _c_i64, _c_vp]),
+    "prox_expert_route_workspace_size": (_c_i32, [_c_i32, _c_i32, _c_i32, _P(_c_size)]),
+    "prox_expert_route": (_c_i32, [_c_vp, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
+                                   _c_vp, _c_size, _c_vp]),
+    "prox_fp8_quantize": (_c_i32, [_c_vp, _c_i32, _c_i32, _c_i32, _c_i64, _c_i32, _c_vp, _c_i64, _c_vp, _c_vp]),
+    "prox_expert_combine": (_c_i32, [_c_vp, _c_i32, _c_i32, _c_i64, _c_vp, _c_vp, _c_i32, _c_i32, _c_i32, _c_vp,
+                                     _c_i32, _c_i64, _c_vp]),
+    "prox_moe_workspace_size": (_c_i32, [_P(prox_moe_layer), _c_i32, _P(_c_size)]),
+    "prox_moe_ffn": (_c_i32, [_P(prox_moe_layer), _c_vp, _c_i32, _c_vp, _c_vp, _c_size, _c_vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _fn = getattr(_lib, _name)
@@ -446,3 +472,195 @@ def prox_set_wait_limit(ticks: int) -> int:
     prev = ctypes.c_uint32(0)
     _check(_lib.prox_set_wait_limit(int(ticks), ctypes.byref(prev)))
     return int(prev.value)
+
+
+# ------------------------------------------------------------- routed FFN
+# These calls check shapes, types and devices here and launch on the tensors'
+# device.  Rows may be strided (the last dimension must be contiguous).
+_EXPERT_TYPES = {torch.float32: PROX_F32, torch.bfloat16: PROX_BF16, torch.float8_e4m3fn: PROX_FP8}
+_OUT_TYPES = {torch.float32: PROX_F32, torch.bfloat16: PROX_BF16}
+
+
+def _dtype_code(t: torch.Tensor, types: dict, name: str) -> int:
+    code = types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} is {t.dtype}, expected one of {', '.join(str(v) for v in types)}")
+    return code
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of a 2-D tensor with contiguous rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
+    s0, s1 = t.stride()
+    rows, cols = t.shape
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if rows <= 1:
+        return cols  # the stride of a single row is not used
+    if s0 < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return s0
+
+
+def _flat(t, shape, dtype, name: str) -> int:
+    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _launch(fn, device: torch.device, tensors, stream, *args) -> None:
+    """fn(*args, stream) with the tensors' device as the current one."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a GPU")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {t.device} and {device} in one call")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+
+
+class ProxExperts:
+    """Weights of a product by expert and their prox_experts descriptor.
+
+    w        [n_groups, n, k] float32, bfloat16 or float8_e4m3fn, k contiguous
+    w_gate   the same shape and strides: gated product, w being the up matrices
+    scale, gate_scale   float8: float32 [n_groups, ceil(n/128), ceil(k/128)]
+    """
+
+    def __init__(self, w: torch.Tensor, w_gate: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                 gate_scale: torch.Tensor | None = None, activation: int = PROX_ACT_SILU):
+        if w.dim() != 3:
+            raise ValueError("w must be [n_groups, n, k]")
+        self.n_groups, self.n, self.k = (int(v) for v in w.shape)
+        self.wdtype = _dtype_code(w, _EXPERT_TYPES, "w")
+        if self.k > 1 and w.stride(2) != 1:
+            raise ValueError("the rows of w must be contiguous")
+        if w_gate is not None and (w_gate.shape != w.shape or w_gate.dtype != w.dtype or w_gate.device != w.device or
+                                   w_gate.stride() != w.stride()):
+            raise ValueError("w_gate must have the shape, strides, type and device of w")
+        blocks = (self.n_groups, -(-self.n // 128), -(-self.k // 128))
+        if (scale is not None) != (self.wdtype == PROX_FP8) or \
+                (gate_scale is not None) != (self.wdtype == PROX_FP8 and w_gate is not None):
+            raise ValueError("float8 weights need a scale for each matrix, other weights take none")
+        for t, name in ((scale, "scale"), (gate_scale, "gate_scale")):
+            if t is not None:
+                _flat(t, blocks, torch.float32, name)
+                if t.device != w.device:
+                    raise ValueError(f"{name} is on {t.device}, w on {w.device}")
+        self.device, self.activation = w.device, activation
+        self.tensors = (w, w_gate, scale, gate_scale)  # keeps the buffers alive
+        row_stride = w.stride(1) if self.n > 1 else self.k
+        group_stride = w.stride(0) if self.n_groups > 1 else 0
+        self.desc = prox_experts(self.n_groups, self.n, self.k, self.wdtype, activation, 0, row_stride, group_stride,
+                                 *(t.data_ptr() if t is not None else None for t in self.tensors))
+        self._ref = ctypes.byref(self.desc)
+
+
+def prox_grouped_matmul(experts: ProxExperts, a: torch.Tensor, out: torch.Tensor, offsets: torch.Tensor | None = None,
+                        row_index: torch.Tensor | None = None, a_scale: torch.Tensor | None = None,
+                        stream=None) -> None:
+    """out[r] = a[row_index[r]] @ experts.w[g].T for the rows r of group g
+    (offsets[g] <= r < offsets[g + 1]); gated experts: up times act(gate)."""
+    rows = out.shape[0]
+    a_stride, out_stride = _row_stride(a, "a"), _row_stride(out, "out")
+    if a.shape[1] != experts.k or _dtype_code(a, _EXPERT_TYPES, "a") != experts.wdtype:
+        raise ValueError(f"a must be [rows, {experts.k}] in the type of the weights, not {a.dtype} {tuple(a.shape)}")
+    if out.shape[1] != experts.n:
+        raise ValueError(f"out must be [rows, {experts.n}], not {tuple(out.shape)}")
+    po = _flat(offsets, (experts.n_groups + 1,), torch.int32, "offsets") if offsets is not None else None
+    pi = _flat(row_index, (rows,), torch.int32, "row_index") if row_index is not None else None
+    ps = None
+    if experts.wdtype == PROX_FP8:
+        if a_scale is None:
+            raise ValueError("float8 rows need a_scale")
+        ps = _flat(a_scale, (a.shape[0], -(-experts.k // 128)), torch.float32, "a_scale")
+    elif a_scale is not None:
+        raise ValueError("a_scale is for float8 rows only")
+    _launch(_lib.prox_grouped_matmul, experts.device, (a, out, offsets, row_index, a_scale), stream,
+            experts._ref, a.data_ptr(), a.shape[0], a_stride, ps, pi, po, rows, out.data_ptr(),
+            _dtype_code(out, _OUT_TYPES, "out"), out_stride)
+
+
+def prox_expert_route_workspace_size(n_tokens: int, n_experts: int, top_k: int) -> int:
+    out = _c_size()
+    _check(_lib.prox_expert_route_workspace_size(n_tokens, n_experts, top_k, ctypes.byref(out)))
+    return int(out.value)
+
+
+def prox_expert_route(logits: torch.Tensor, expert_idx: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
+                      row_token: torch.Tensor, row_of: torch.Tensor, ws: torch.Tensor, renormalize: bool = True,
+                      stream=None) -> None:
+    """The top_k experts of every token (top_k: the columns of expert_idx),
+    their weights, and the rows by expert."""
+    if logits.dim() != 2 or expert_idx.dim() != 2 or not logits.is_contiguous():
+        raise ValueError("logits must be contiguous [tokens, experts], expert_idx [tokens, top_k]")
+    t, e = logits.shape
+    k = expert_idx.shape[1]
+    i32 = torch.int32
+    _launch(_lib.prox_expert_route, logits.device, (expert_idx, weight, offsets, row_token, row_of, ws), stream,
+            logits.data_ptr(), _dtype_code(logits, _OUT_TYPES, "logits"), t, e, k, int(bool(renormalize)),
+            _flat(expert_idx, (t, k), i32, "expert_idx"), _flat(weight, (t, k), torch.float32, "weight"),
+            _flat(offsets, (e + 1,), i32, "offsets"), _flat(row_token, (t * k,), i32, "row_token"),
+            _flat(row_of, (t, k), i32, "row_of"), _ptr(ws), ws.numel() * ws.element_size())
+
+
+def prox_fp8_quantize(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1, stream=None) -> None:
+    """q = e4m3(x / scale), scale = amax / 448 of each block_rows x 128 block."""
+    xs, qs = _row_stride(x, "x"), _row_stride(q, "q")
+    rows, k = x.shape
+    if q.shape != x.shape or q.dtype != torch.float8_e4m3fn:
+        raise ValueError("q must be float8_e4m3fn of the shape of x")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    _launch(_lib.prox_fp8_quantize, x.device, (q, scale), stream, x.data_ptr(), _dtype_code(x, _OUT_TYPES, "x"), rows,
+            k, xs, block_rows, q.data_ptr(), qs,
+            _flat(scale, (-(-rows // block_rows), -(-k // 128)), torch.float32, "scale"))
+
+
+def prox_expert_combine(h: torch.Tensor, row_of: torch.Tensor, weight: torch.Tensor, y: torch.Tensor,
+                        stream=None) -> None:
+    """y[t] = sum over slots s of weight[t, s] * h[row_of[t, s]]."""
+    hs, ys = _row_stride(h, "h"), _row_stride(y, "y")
+    if row_of.dim() != 2 or y.shape != (row_of.shape[0], h.shape[1]):
+        raise ValueError("row_of must be [tokens, top_k] and y [tokens, columns of h]")
+    t, k = row_of.shape
+    _launch(_lib.prox_expert_combine, h.device, (row_of, weight, y), stream, h.data_ptr(),
+            _dtype_code(h, _OUT_TYPES, "h"), h.shape[0], hs, _flat(row_of, (t, k), torch.int32, "row_of"),
+            _flat(weight, (t, k), torch.float32, "weight"), t, k, h.shape[1], y.data_ptr(),
+            _dtype_code(y, _OUT_TYPES, "y"), ys)
+
+
+class ProxMoeLayer:
+    """A routed FFN layer: router [n_experts, d_model], gated up/gate experts
+    [n_experts, d_ff, d_model] and down experts [n_experts, d_model, d_ff]."""
+
+    def __init__(self, w_router: torch.Tensor, up: ProxExperts, down: ProxExperts, top_k: int, renormalize: bool = True):
+        want = torch.float32 if up.wdtype == PROX_F32 else torch.bfloat16
+        _flat(w_router, (up.n_groups, up.k), want, "w_router")
+        if up.device != w_router.device or down.device != w_router.device:
+            raise ValueError("the layer's weights are on different devices")
+        self.w_router, self.up, self.down, self.top_k = w_router, up, down, top_k
+        self.x_dtype, self.device = want, w_router.device
+        self.desc = prox_moe_layer(up.desc, down.desc, w_router.data_ptr(), top_k, int(bool(renormalize)), 0)
+        prox_moe_workspace_size(self, 1)  # the library's own checks of the layer
+
+
+def prox_moe_workspace_size(layer: ProxMoeLayer, n_tokens: int) -> int:
+    out = _c_size()
+    _check(_lib.prox_moe_workspace_size(ctypes.byref(layer.desc), n_tokens, ctypes.byref(out)))
+    return int(out.value)
+
+
+def prox_moe_ffn(layer: ProxMoeLayer, x: torch.Tensor, y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """y = the routed FFN of x ([tokens, d_model] in layer.x_dtype); y float32."""
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, d_model]")
+    shape = (x.shape[0], layer.up.k)
+    _launch(_lib.prox_moe_ffn, layer.device, (x, y, ws), stream, ctypes.byref(layer.desc),
+            _flat(x, shape, layer.x_dtype, "x"), shape[0], _flat(y, shape, torch.float32, "y"), _ptr(ws),
+            ws.numel() * ws.element_size())

@@ -59,7 +59,9 @@ typedef enum {
   PROX_ERR_INTERNAL = -4
 } prox_status;
 
-typedef enum { PROX_F32 = 0, PROX_BF16 = 1 } prox_dtype;
+/* PROX_FP8 (e4m3, OCP "fn" form: largest value 448, NaN 0x7F) is a type of the
+ * routed-FFN products only. */
+typedef enum { PROX_F32 = 0, PROX_BF16 = 1, PROX_FP8 = 2 } prox_dtype;
 
 /*
  * One packed FFN layer.  A plain descriptor of caller-owned device buffers;
@@ -425,6 +427,177 @@ prox_status prox_ffn_stage2(const prox_layer* layer, const void* x, int32_t batc
 prox_status prox_proxy_state(const prox_layer* layer, const void* x, int32_t batch,
                              float tau_x, float* s_tilde, int32_t* in_count, void* ws,
                              size_t ws_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Routed FFN: a layer whose FFN is split into experts, each a SwiGLU / GeGLU
+ * FFN of its own.  A router sends every token to the top_k experts with the
+ * largest logits; the rows of one expert run through that expert's matrices,
+ * and a token's rows are added up with the router's weights:
+ *   prox_expert_route    logits -> experts, weights, rows listed by expert
+ *   prox_grouped_matmul  ragged products by expert (plain or gated)
+ *   prox_fp8_quantize    rows or weights to e4m3 with block scales
+ *   prox_expert_combine  y[t] = sum_s weight[t][s] h[row_of[t][s]]
+ *   prox_moe_ffn         all of it for one layer
+ * No thresholds and no proxy: every channel of the chosen experts is computed.
+ * Sums, softmax and scales are fp32; a result in a 16-bit type is rounded once,
+ * to nearest even.  Results do not depend on the launch: calls with the same
+ * arguments give the same bits.  The device must be the current one.  Buffers
+ * that a call writes must not overlap the ones it reads.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Weights of n_groups products (experts), row j of group g at
+ *   w + (g * group_stride + j * row_stride) elements, k contiguous values.
+ * w       [n_groups][n][k] in wdtype (PROX_F32, PROX_BF16 or PROX_FP8), the
+ *         orientation [outputs][inputs] of a linear layer.  16-byte aligned;
+ *         k and both strides are multiples of 16 bytes.  row_stride >= k;
+ *         group_stride may be any multiple (0: all groups share one matrix).
+ * w_gate  NULL: plain product.  Else the gate matrices, with the same strides:
+ *         out = (a w^T) * act(a w_gate^T), w being the up matrices.  The
+ *         w_upgate_t buffer of a prox_layer is such a pair (w = w_upgate_t,
+ *         w_gate = w + d_model, row_stride = 2 * d_model, one group).
+ * w_scale, w_gate_scale
+ *         PROX_FP8 only: fp32 [n_groups][ceil(n/128)][ceil(k/128)], contiguous;
+ *         a weight stands for its e4m3 value times its 128 x 128 block's scale.
+ * activation  prox_activation, gated products only.
+ * reserved    must be 0.
+ * 1 <= n_groups <= 1024, n and k at most 2^24.
+ */
+typedef struct {
+  int32_t n_groups, n, k;
+  int32_t wdtype;
+  int32_t activation;
+  int32_t reserved;
+  int64_t row_stride, group_stride; /* elements */
+  const void* w;
+  const void* w_gate;
+  const float* w_scale;
+  const float* w_gate_scale;
+} prox_experts;
+
+/*
+ * Ragged products: for every group g and row offsets[g] <= r < offsets[g+1],
+ *   out[r][j] = sum_k a[src(r)][k] w_g[j][k]      (gated: see prox_experts)
+ * a          device [a_rows][k] in experts->wdtype, rows a_stride elements
+ *            apart (a multiple of 16 bytes), 16-byte aligned
+ * a_scale    PROX_FP8: device fp32 [a_rows][ceil(k/128)], the scale of each 128
+ *            inputs of a row (prox_fp8_quantize, block_rows 1); else ignored
+ * row_index  device [rows] int32: src(r) = row_index[r]; an index outside
+ *            [0, a_rows) stands for a row of zeros.  NULL: src(r) = r
+ * offsets    device [n_groups + 1] int32, ascending, offsets[0] >= 0 and
+ *            offsets[n_groups] <= rows (values outside [0, rows] are clamped).
+ *            Groups may be empty.  NULL: one group of all rows (n_groups 1)
+ * rows       rows of out, known to the host: an upper bound of what offsets
+ *            hold.  0 is allowed (nothing is done)
+ * out        device [rows][n] of out_dtype (PROX_F32 or PROX_BF16), rows
+ *            out_stride elements apart.  Rows that belong to no group are left
+ *            as they were
+ * PROX_FP8 products are those of the matrix cores: of eight neighbouring k, each
+ * product is cut off at 2^-13 of the largest one's power of two; the eights and
+ * the blocks of 128 are added in fp32.
+ * The offsets are read on the device: no host synchronisation, and a captured
+ * call may be replayed with other offsets and row indices.  No workspace.
+ * Asynchronous.
+ */
+prox_status prox_grouped_matmul(const prox_experts* experts, const void* a, int32_t a_rows, int64_t a_stride,
+                                const float* a_scale, const int32_t* row_index, const int32_t* offsets, int32_t rows,
+                                void* out, int32_t out_dtype, int64_t out_stride, void* stream);
+
+/*
+ * Router: per token the top_k experts by logit, ties to the lowest expert, and
+ * their softmax weights; and the rows listed by expert (tokens ascending within
+ * one), as prox_grouped_matmul and prox_expert_combine take them.
+ *   logits       device [n_tokens][n_experts], PROX_F32 or PROX_BF16.  -inf: the
+ *                expert is not chosen; a token may have fewer than top_k experts
+ *                left, or none.  +inf counts as the largest finite fp32 value.
+ *                NaN comes before every number, and the token's weights are NaN
+ *   renormalize  1: softmax over the chosen experts; 0: over all experts
+ *   expert_idx   device [n_tokens][top_k] int32, by descending logit; -1 in the
+ *                slots that no expert fills
+ *   weight       device [n_tokens][top_k] fp32, 0 in those slots
+ *   offsets      device [n_experts + 1] int32: expert e has the rows
+ *                offsets[e] .. offsets[e+1] - 1
+ *   row_token    device [n_tokens * top_k] int32: the token of each row; -1
+ *                behind the last row
+ *   row_of       device [n_tokens][top_k] int32: the row of each slot, or -1
+ *   ws           device, >= prox_expert_route_workspace_size bytes, 256-byte
+ *                aligned, no zeroing needed
+ * 1 <= top_k <= min(n_experts, 32), n_experts <= 1024, n_tokens * top_k <= 2^30;
+ * n_tokens 0 gives zero offsets.  Asynchronous.
+ */
+prox_status prox_expert_route_workspace_size(int32_t n_tokens, int32_t n_experts, int32_t top_k, size_t* bytes);
+prox_status prox_expert_route(const void* logits, int32_t logits_dtype, int32_t n_tokens, int32_t n_experts,
+                              int32_t top_k, int32_t renormalize, int32_t* expert_idx, float* weight, int32_t* offsets,
+                              int32_t* row_token, int32_t* row_of, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Quantizer to e4m3 with one fp32 scale per block of block_rows x 128 values:
+ *   scale = fp32(amax / 448), amax the block's largest |x|
+ *   q     = e4m3(fp32(x / scale)), to nearest, ties to even
+ * An all-zero block has scale 0 and codes 0; a block that holds an infinity or
+ * NaN has scale NaN and codes NaN.
+ *   x           device [rows][k], PROX_F32 or PROX_BF16, rows x_stride elements
+ *               apart; x and its rows 16-byte aligned, k a multiple of 16
+ *   block_rows  1 (activations) or 128 (weights; the last block may have fewer
+ *               rows).  The rows of several matrices [g][n][k] may be quantized
+ *               in one call if n is a multiple of 128
+ *   q           device [rows][k] bytes, rows q_stride apart, 16-byte aligned
+ *   scale       device [ceil(rows / block_rows)][ceil(k / 128)] fp32
+ * Asynchronous.
+ */
+prox_status prox_fp8_quantize(const void* x, int32_t x_dtype, int32_t rows, int32_t k, int64_t x_stride,
+                              int32_t block_rows, void* q, int64_t q_stride, float* scale, void* stream);
+
+/*
+ * y[t][j] = sum over the slots s = 0 .. top_k - 1, in this order, of
+ *   weight[t][s] * h[row_of[t][s]][j]
+ * in fp32; a slot whose row lies outside [0, h_rows) adds nothing.
+ *   h       device [h_rows][n], PROX_F32 or PROX_BF16, rows h_stride apart
+ *   row_of  device [n_tokens][top_k] int32
+ *   weight  device [n_tokens][top_k] fp32
+ *   y       device [n_tokens][n] of y_dtype (PROX_F32 or PROX_BF16, overwritten),
+ *           rows y_stride elements apart
+ * 1 <= top_k <= 32.  Asynchronous.
+ */
+prox_status prox_expert_combine(const void* h, int32_t h_dtype, int32_t h_rows, int64_t h_stride,
+                                const int32_t* row_of, const float* weight, int32_t n_tokens, int32_t top_k, int32_t n,
+                                void* y, int32_t y_dtype, int64_t y_stride, void* stream);
+
+/*
+ * One routed layer: w_router [n_experts][d_model] (contiguous, 16-byte aligned;
+ * PROX_F32 for fp32 layers, PROX_BF16 for bf16 and fp8 ones), up a gated
+ * [n_experts][d_ff][d_model], down a plain [n_experts][d_model][d_ff].
+ */
+typedef struct {
+  prox_experts up;
+  prox_experts down;
+  const void* w_router;
+  int32_t top_k;
+  int32_t renormalize; /* as in prox_expert_route */
+  int32_t reserved;    /* must be 0 */
+} prox_moe_layer;
+
+/* Workspace bytes of prox_moe_ffn for n_tokens tokens. */
+prox_status prox_moe_workspace_size(const prox_moe_layer* layer, int32_t n_tokens, size_t* bytes);
+
+/*
+ * One pass through a routed FFN layer:
+ *   logits = x w_router^T (kept in fp32); experts and weights by
+ *   prox_expert_route; y[t] = sum_s weight[t][s] down_e(up_e(x[t])).
+ *   x   device [n_tokens][d_model], contiguous, PROX_F32 for fp32 layers,
+ *       PROX_BF16 for bf16 and fp8 ones (an fp8 layer quantizes x, and the rows
+ *       between its products, with prox_fp8_quantize)
+ *   y   device [n_tokens][d_model] fp32 (overwritten)
+ *   ws  device, >= prox_moe_workspace_size bytes, 256-byte aligned, no zeroing
+ *       needed
+ * The rows between the products are stored in x's type.  n_tokens >= 0, for a
+ * prompt or a decode batch alike.  x and y 16-byte aligned.  Asynchronous; may be
+ * captured (calls that overlap in time need workspaces of their own).
+ */
+prox_status prox_moe_ffn(const prox_moe_layer* layer, const void* x, int32_t n_tokens, float* y, void* ws,
+                         size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

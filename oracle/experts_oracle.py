@@ -1,0 +1,129 @@
+"""Plain NumPy fp64 definitions of the routed-FFN operators (test infrastructure
+only; shares no code with the library)."""
+from __future__ import annotations
+
+import numpy as np
+
+FLT_MAX = float(np.finfo(np.float32).max)
+
+
+def route(logits: np.ndarray, top_k: int, renormalize: bool = True) -> dict:
+    """Experts by (logit descending, expert ascending); NaN before every number,
+    -inf never chosen, +inf as the largest finite fp32 value."""
+    z = np.asarray(logits, dtype=np.float64)
+    T, E = z.shape
+    idx = np.full((T, top_k), -1, np.int32)
+    weight = np.zeros((T, top_k), np.float64)
+    rows = [[] for _ in range(E)]
+    for t in range(T):
+        row = np.minimum(z[t], FLT_MAX)
+        rank = [(-np.inf if np.isnan(v) else -v, e) for e, v in enumerate(row) if np.isnan(v) or v > -np.inf]
+        chosen = [e for _, e in sorted(rank)[:top_k]]
+        if not chosen:
+            continue
+        top = row[chosen[0]]
+        with np.errstate(under="ignore"):
+            p = np.exp(row - top)
+        total = p[chosen].sum() if renormalize else p[[e for _, e in rank]].sum()
+        for s, e in enumerate(chosen):
+            idx[t, s] = e
+            weight[t, s] = p[e] / total
+            rows[e].append((t, s))
+    offsets = np.zeros(E + 1, np.int32)
+    row_token = np.full(T * top_k, -1, np.int32)
+    row_of = np.full((T, top_k), -1, np.int32)
+    r = 0
+    for e in range(E):
+        for t, s in rows[e]:
+            row_token[r], row_of[t, s] = t, r
+            r += 1
+        offsets[e + 1] = r
+    return {"idx": idx, "weight": weight, "offsets": offsets, "row_token": row_token, "row_of": row_of}
+
+
+def round_e4m3(v: np.ndarray) -> np.ndarray:
+    """Nearest e4m3 value, ties to even, for |v| <= 448 (fp64 in, fp64 out)."""
+    a = np.abs(v)
+    with np.errstate(divide="ignore"):
+        e = np.floor(np.log2(np.maximum(a, 2.0 ** -6)))
+    step = np.exp2(e - 3)
+    return np.copysign(np.rint(a / step) * step, v)
+
+
+def quantize(x: np.ndarray, block_rows: int):
+    """(values of the codes, scales): scale = fp32(amax / 448), code =
+    e4m3(fp32(x / scale)), per block_rows x 128 block of fp32 x."""
+    x = np.asarray(x, np.float32)
+    R, K = x.shape
+    scale = np.zeros((-(-R // block_rows), -(-K // 128)), np.float32)
+    q = np.zeros((R, K), np.float64)
+    for i in range(scale.shape[0]):
+        for j in range(scale.shape[1]):
+            b = (slice(i * block_rows, (i + 1) * block_rows), slice(j * 128, (j + 1) * 128))
+            amax = np.max(np.abs(x[b]))
+            if not np.isfinite(amax):
+                scale[i, j], q[b] = np.nan, np.nan
+                continue
+            scale[i, j] = amax / np.float32(448.0)
+            if scale[i, j] > 0:
+                q[b] = round_e4m3((x[b] / scale[i, j]).astype(np.float64))
+    return q, scale
+
+
+def widen_scale(scale: np.ndarray, block_rows: int, rows: int, k: int) -> np.ndarray:
+    s = np.repeat(np.asarray(scale, np.float64), 128, axis=-1)[..., :k]
+    return np.repeat(s, block_rows, axis=-2)[..., :rows, :]
+
+
+def act(z: np.ndarray, kind: int) -> np.ndarray:
+    if kind == 1:
+        return 0.5 * z * (1.0 + np.tanh(np.sqrt(2.0 / np.pi) * (z + 0.044715 * z ** 3)))
+    with np.errstate(over="ignore"):
+        return z / (1.0 + np.exp(-z))
+
+
+def _largest_of_8(w, x):
+    """Per row of w, the sum over eight neighbouring k of the largest |w x|."""
+    p = np.pad(np.abs(w) * np.abs(x), ((0, 0), (0, -w.shape[1] % 8)))
+    return p.reshape(w.shape[0], -1, 8).max(axis=2).sum(axis=1)
+
+
+def grouped(a, w, offsets, row_index=None, rows=None, w_gate=None, activation=0, eights=0.0):
+    """(out, mag): out as defined, and for the error bound the sum of the
+    magnitudes of the products behind each value (a pair for gated products,
+    with the gate's value).  Rows outside every group are NaN.  eights: that much
+    of _largest_of_8 is added to the magnitudes."""
+    rows = (len(row_index) if row_index is not None else a.shape[0]) if rows is None else rows
+    G, n, _ = w.shape
+    out = np.full((rows, n), np.nan)
+    mag = [np.zeros((rows, n)) for _ in range(4)]
+    for g in range(G):
+        for r in range(offsets[g], offsets[g + 1]):
+            s = r if row_index is None else row_index[r]
+            x = a[s] if 0 <= s < a.shape[0] else np.zeros(a.shape[1])
+            u = w[g] @ x
+            mag[0][r], mag[1][r] = np.abs(w[g]) @ np.abs(x), u
+            if eights:
+                mag[0][r] += eights * _largest_of_8(w[g], x)
+            if w_gate is None:
+                out[r] = u
+            else:
+                z = w_gate[g] @ x
+                mag[2][r], mag[3][r] = np.abs(w_gate[g]) @ np.abs(x), z
+                if eights:
+                    mag[2][r] += eights * _largest_of_8(w_gate[g], x)
+                out[r] = u * act(z, activation)
+    return out, mag
+
+
+def combine(h, row_of, weight):
+    """(y, mag): the weighted sums and the sums of magnitudes."""
+    T, k = row_of.shape
+    y, mag = np.zeros((T, h.shape[1])), np.zeros((T, h.shape[1]))
+    for t in range(T):
+        for s in range(k):
+            r = row_of[t, s]
+            if 0 <= r < h.shape[0]:
+                y[t] += weight[t, s] * h[r]
+                mag[t] += np.abs(weight[t, s] * h[r])
+    return y, mag
