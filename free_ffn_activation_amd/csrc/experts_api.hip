@@ -32,6 +32,8 @@ prox_status check_experts(const prox_experts* e) {
   const int es = elem(e->wdtype);
   if (static_cast<int64_t>(e->k) * es % 16 != 0 || e->row_stride * es % 16 != 0 || e->group_stride * es % 16 != 0)
     return fail(PROX_ERR_UNSUPPORTED, "experts k and strides must be multiples of 16 bytes");
+  if (e->row_stride * es >= (1 << 23))
+    return fail(PROX_ERR_UNSUPPORTED, "experts row_stride must be below 8 MiB");
   if (e->row_stride < e->k || e->group_stride < 0)
     return fail(PROX_ERR_INVALID_ARG, "experts row_stride is below k or group_stride is negative");
   if (!e->w || !aligned(e->w, 16) || !aligned(e->w_gate, 16))
@@ -170,6 +172,7 @@ PROX_API prox_status prox_grouped_matmul(const prox_experts* e, const void* a, i
       return fail(PROX_ERR_INVALID_ARG, "a_stride below k or out_stride below n");
     if (a_stride * es % 16 != 0) return fail(PROX_ERR_UNSUPPORTED, "a_stride must be a multiple of 16 bytes");
     if (rows == 0) return PROX_OK;
+    if (a_rows == 0) return fail(PROX_ERR_INVALID_ARG, "a_rows is 0 with %d rows", rows);
     if (!a || !out || (e->wdtype == PROX_FP8 && !a_scale))
       return fail(PROX_ERR_INVALID_ARG, "a, out and (PROX_FP8) a_scale must be non-NULL");
     if (!aligned(a, 16) || !aligned(out, elem(out_dtype)) || !aligned(a_scale, 4) || !aligned(row_index, 4) ||

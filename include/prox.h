@@ -452,7 +452,7 @@ prox_status prox_proxy_state(const prox_layer* layer, const void* x, int32_t bat
  *   w + (g * group_stride + j * row_stride) elements, k contiguous values.
  * w       [n_groups][n][k] in wdtype (PROX_F32, PROX_BF16 or PROX_FP8), the
  *         orientation [outputs][inputs] of a linear layer.  16-byte aligned;
- *         k and both strides are multiples of 16 bytes.  row_stride >= k;
+ *         k and both strides are multiples of 16 bytes.  row_stride >= k, below 8 MiB;
  *         group_stride may be any multiple (0: all groups share one matrix).
  * w_gate  NULL: plain product.  Else the gate matrices, with the same strides:
  *         out = (a w^T) * act(a w_gate^T), w being the up matrices.  The
@@ -485,7 +485,7 @@ typedef struct {
  * a_scale    PROX_FP8: device fp32 [a_rows][ceil(k/128)], the scale of each 128
  *            inputs of a row (prox_fp8_quantize, block_rows 1); else ignored
  * row_index  device [rows] int32: src(r) = row_index[r]; an index outside
- *            [0, a_rows) stands for a row of zeros.  NULL: src(r) = r
+ *            [0, a_rows) gives a row of zeros in out.  NULL: src(r) = r
  * offsets    device [n_groups + 1] int32, ascending, offsets[0] >= 0 and
  *            offsets[n_groups] <= rows (values outside [0, rows] are clamped).
  *            Groups may be empty.  NULL: one group of all rows (n_groups 1)
