@@ -13,6 +13,8 @@
 // place c ^ (r % 8), so that the eight rows of a fragment read touch all banks.
 // The order of k inside a step does not matter as long as both sides agree, so
 // all three types read the same two 16-byte chunks per lane and step.
+#include <stdlib.h>
+
 #include "experts_internal.h"
 #include "prox_device.h"
 
@@ -82,6 +84,11 @@ __device__ __forceinline__ void copy16(const void* src, uint32_t to) {
 __device__ __forceinline__ void copy16(const uint8_t* base, uint32_t offset, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base)
                : "m0");
+}
+
+// 4 bytes per lane, to LDS at `to` + 4 * lane.
+__device__ __forceinline__ void copy4(const void* src, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(src) : "m0");
 }
 
 struct Item {
@@ -179,17 +186,19 @@ __device__ __forceinline__ void wait_copies_and_meet() {
 }
 
 // One block: BT tokens x BC weight rows (gated: BC / 2 channels, up and gate in
-// turn by sixteen rows), WC x WT waves.  Two LDS buffers: while the waves
-// multiply step s, the copies of step s + 1 are under way.
-template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC>
+// turn by sixteen rows), WC x WT waves, S LDS buffers: while the waves multiply
+// step s, the copies of steps s + 1 .. s + S - 1 are under way.
+template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC, int S>
 __global__ void __launch_bounds__(64 * WT * WC) grouped_kernel(GroupedArgs a) {
   constexpr int kWaves = WT * WC, FC = BC / 16 / WC, FT = BT / 16 / WT;  // fragments of 16 per wave
   constexpr int NW = BC / 8 / kWaves, NX = BT / 8 / kWaves;              // copies per wave and step
   constexpr bool kFp8 = std::is_same<T, Fp8Tag>::value;
+  constexpr uint32_t kBuffer = (BC + BT) * 128 + (kFp8 ? kWaves * 256 : 0);
+  constexpr int kCopies = NW + NX + (kFp8 ? 1 : 0);
   static_assert(NW * 8 * kWaves == BC && NX * 8 * kWaves == BT && FC * 16 * WC == BC && FT * 16 * WT == BT, "tile");
   static_assert(FC <= 8 && 128 % (FC * 16) == 0, "a wave's channels lie in one scale block");
   static_assert(!kGated || FC % 2 == 0, "up and gate of a channel belong to one wave");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (BC + BT) * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[S * kBuffer];
   __shared__ Item s_item;
   __shared__ int s_total[kWaves];
   const int chan_per_tile = kGated ? BC / 2 : BC;
@@ -226,18 +235,20 @@ __global__ void __launch_bounds__(64 * WT * WC) grouped_kernel(GroupedArgs a) {
 #pragma unroll
   for (int i = 0; i < NX; ++i)
     xsrc[i] = a.a + max(source((i * kWaves + wave) * 8 + crow), 0) * a.a_stride + chunk * 16;
-  // fp8: the scales of this lane's tokens and of this wave's channels, which
-  // lie in one block of 128 (up and gate each)
-  const float* xs[FT];
-  const float *wsc_up = nullptr, *wsc_gate = nullptr;
+  // fp8: each step brings the scales of the tile's tokens (64 a wave) and of its
+  // channels (the wave after those: lane l the l-th block of 128, up then gate)
+  // into LDS by one copy per wave, whose lanes without a scale repeat another
+  constexpr int kTokenWaves = (BT + 63) / 64, kBlocks = BC / (kGated ? 256 : 128) + 1;
+  static_assert(!kFp8 || kTokenWaves < kWaves, "a wave is left for the channels' scales");
+  const float* scale_src = nullptr;
   if constexpr (kFp8) {
-#pragma unroll
-    for (int t = 0; t < FT; ++t)
-      xs[t] = a.a_scale + static_cast<int64_t>(max(source((wt * FT + t) * 16 + (lane & 15)), 0)) * a.kblocks;
-    const int j = min(c0 + wc * FC * (kGated ? 8 : 16), a.n - 1);
-    const int64_t block = (static_cast<int64_t>(it.group) * a.nblocks + j / kScaleBlock) * a.kblocks;
-    wsc_up = a.w_scale + block;
-    wsc_gate = kGated ? a.w_gate_scale + block : wsc_up;
+    if (wave < kTokenWaves) {
+      scale_src = a.a_scale + static_cast<int64_t>(max(source(wave * 64 + lane), 0)) * a.kblocks;
+    } else {
+      const int block = min(c0 / kScaleBlock + lane % kBlocks, a.nblocks - 1);
+      scale_src = (kGated && (lane / kBlocks & 1) ? a.w_gate_scale : a.w_scale) +
+                  (static_cast<int64_t>(it.group) * a.nblocks + block) * a.kblocks;
+    }
   }
 
   f32x4_t acc[FC][FT];
@@ -246,76 +257,120 @@ __global__ void __launch_bounds__(64 * WT * WC) grouped_kernel(GroupedArgs a) {
 #pragma unroll
     for (int t = 0; t < FT; ++t) acc[f][t] = f32x4_t{0, 0, 0, 0};
 
-  constexpr uint32_t kBuffer = (BC + BT) * 128;
+  constexpr uint32_t kScales = (BC + BT) * 128;  // their place in a buffer
   const uint32_t lds0 = lds_offset(lds);
-  const auto copy = [&](int kb, uint32_t to) {
+  // copy i of the step at byte kb of the rows.  Chunks past the end of k (in the
+  // last step only) repeat the step's first one; multiply() takes zeros there.
+  const auto copy = [&](int i, int kb, int lane_kb, uint32_t to) {
     to += lds0 + wave * 1024;
-    if (kb + 128 <= a.kbytes) {
-#pragma unroll
-      for (int i = 0; i < NW; ++i)  // copy i holds up (even sixteens) or gate rows
-        copy16((kGated && (((i * kWaves + wave) >> 1) & 1) ? w_gate : w_up) + kb, woff[i], to + i * (kWaves * 1024));
-#pragma unroll
-      for (int i = 0; i < NX; ++i) copy16(xsrc[i] + kb, to + BC * 128 + i * (kWaves * 1024));
-    } else {  // the last step of a k that is no multiple of 128 bytes
-      const bool in = kb + chunk * 16 < a.kbytes;
-#pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        const uint8_t* w = (kGated && (((i * kWaves + wave) >> 1) & 1) ? w_gate : w_up) + kb + woff[i];
-        copy16(in ? static_cast<const void*>(w) : &g_zero16, to + i * (kWaves * 1024));
-      }
-#pragma unroll
-      for (int i = 0; i < NX; ++i)
-        copy16(in ? static_cast<const void*>(xsrc[i] + kb) : &g_zero16, to + BC * 128 + i * (kWaves * 1024));
+    if (i < NW) {  // up (even sixteens of rows) or gate
+      copy16((kGated && (((i * kWaves + wave) >> 1) & 1) ? w_gate : w_up), woff[i] + lane_kb,
+             to + i * (kWaves * 1024));
+    } else if (i < NW + NX) {
+      copy16(xsrc[i - NW] + lane_kb, to + BC * 128 + (i - NW) * (kWaves * 1024));
+    } else if constexpr (kFp8) {
+      copy4(scale_src + (kb >> 7), to - wave * 768 + kScales);
     }
   };
+  const auto lane_offset = [&](int kb) { return kb + chunk * 16 < a.kbytes ? kb : kb - chunk * 16; };
   const int row = lane & 15, quad = lane >> 4;
   const int place0 = ((quad) ^ (row & 7)) << 4, place1 = ((4 + quad) ^ (row & 7)) << 4;
-  const auto multiply = [&](int kb, const uint8_t* from) {
+  // the block of 128 channels that this wave's lie in, from the tile's first on
+  const int block = (c0 + wc * FC * (kGated ? 8 : 16)) / kScaleBlock - c0 / kScaleBlock;
+  // Multiplies the step in `from`, and meanwhile (more) issues the copies of the
+  // step at next_kb into `to`, a few between the products.
+  const auto multiply = [&](auto more, auto tail, int kb, const uint8_t* from, int next_kb, uint32_t to) {
     const uint8_t* pw = from + (wc * FC * 16 + row) * 128;
     const uint8_t* px = from + BC * 128 + (wt * FT * 16 + row) * 128;
+    const auto read = [&](const uint8_t* p) {
+      Frag r;
+      r.c[0] = *reinterpret_cast<const u32x4_t*>(p + place0);
+      r.c[1] = *reinterpret_cast<const u32x4_t*>(p + place1);
+      if constexpr (decltype(tail)::value) {
+        if (kb + quad * 16 >= a.kbytes) r.c[0] = u32x4_t{0, 0, 0, 0};
+        if (kb + quad * 16 + 64 >= a.kbytes) r.c[1] = u32x4_t{0, 0, 0, 0};
+      }
+      return r;
+    };
     Frag xf[FT], wf[2];
+    wf[0] = read(pw);
+#pragma unroll
+    for (int t = 0; t < FT; ++t) xf[t] = read(px + t * 2048);
     float xscale[FT], ws_up = 0.f, ws_gate = 0.f;
+    f32x4_t part[2][FT];  // fp8: a step's products, scaled and added one fragment later
     if constexpr (kFp8) {
+      const float* ps = reinterpret_cast<const float*>(from + kScales);
 #pragma unroll
-      for (int t = 0; t < FT; ++t) xscale[t] = xs[t][kb >> 7];
-      ws_up = wsc_up[kb >> 7];
-      ws_gate = kGated ? wsc_gate[kb >> 7] : ws_up;
+      for (int t = 0; t < FT; ++t) xscale[t] = ps[(wt * FT + t) * 16 + row];
+      ws_up = ps[kTokenWaves * 64 + block];
+      ws_gate = kGated ? ps[kTokenWaves * 64 + kBlocks + block] : ws_up;
     }
-    wf[0].c[0] = *reinterpret_cast<const u32x4_t*>(pw + place0);
-    wf[0].c[1] = *reinterpret_cast<const u32x4_t*>(pw + place1);
+    const auto add = [&](int f) {
 #pragma unroll
-    for (int t = 0; t < FT; ++t) {
-      xf[t].c[0] = *reinterpret_cast<const u32x4_t*>(px + t * 2048 + place0);
-      xf[t].c[1] = *reinterpret_cast<const u32x4_t*>(px + t * 2048 + place1);
-    }
+      for (int t = 0; t < FT; ++t) {
+        const float sc = xscale[t] * (kGated && (f & 1) ? ws_gate : ws_up);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(part[f & 1][t][i], sc, acc[f][t][i]);
+      }
+    };
+    const int lane_kb = lane_offset(next_kb);
 #pragma unroll
     for (int f = 0; f < FC; ++f) {
       // the next channels' fragment is read while this one is multiplied
-      if (f + 1 < FC) {
-        wf[(f + 1) & 1].c[0] = *reinterpret_cast<const u32x4_t*>(pw + (f + 1) * 2048 + place0);
-        wf[(f + 1) & 1].c[1] = *reinterpret_cast<const u32x4_t*>(pw + (f + 1) * 2048 + place1);
+      if (f + 1 < FC) wf[(f + 1) & 1] = read(pw + (f + 1) * 2048);
+      if constexpr (decltype(more)::value) {
+#pragma unroll
+        for (int i = f * kCopies / FC; i < (f + 1) * kCopies / FC; ++i) copy(i, next_kb, lane_kb, to);
       }
 #pragma unroll
       for (int t = 0; t < FT; ++t) {
-        if constexpr (kFp8) {
-          const f32x4_t part = mma<T>(wf[f & 1], xf[t], f32x4_t{0, 0, 0, 0});
-          const float sc = xscale[t] * (kGated && (f & 1) ? ws_gate : ws_up);
+        if constexpr (kFp8) part[f & 1][t] = mma<T>(wf[f & 1], xf[t], f32x4_t{0, 0, 0, 0});
+        else acc[f][t] = mma<T>(wf[f & 1], xf[t], acc[f][t]);
+      }
+      if constexpr (kFp8) {
+        if (f > 0) {
+          add(f - 1);
+          // a matrix instruction, then the four sums that fit beside it
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(part[i], sc, acc[f][t][i]);
-        } else {
-          acc[f][t] = mma<T>(wf[f & 1], xf[t], acc[f][t]);
+          for (int t = 0; t < FT; ++t) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (kFp8) add(FC - 1);
   };
-  copy(0, 0);
-  uint32_t now = 0;
-  for (int kb = 0; kb < a.kbytes; kb += 128) {
+  uint32_t now = 0, next = 0;  // the buffers of this step and of the next copy
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) {
+    if (i * 128 < a.kbytes) {
+      const int lane_kb = lane_offset(i * 128);
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) copy(c, i * 128, lane_kb, next);
+    }
+    next += kBuffer;
+  }
+  const auto advance = [&] {
+    next = next == (S - 1) * kBuffer ? 0 : next + kBuffer;
+    now = now == (S - 1) * kBuffer ? 0 : now + kBuffer;
+  };
+  int kb = 0;
+  for (; kb + (S - 1) * 128 < a.kbytes; kb += 128) {
+    // this step's copies are done when only those of the later steps are left
+    wait_copies_and_meet<(S - 2) * kCopies>();
+    multiply(std::true_type{}, std::false_type{}, kb, lds + now, kb + (S - 1) * 128, next);
+    advance();
+  }
+  for (; kb + 128 <= a.kbytes; kb += 128) {
     wait_copies_and_meet<0>();
-    if (kb + 128 < a.kbytes) copy(kb + 128, now ^ kBuffer);
-    multiply(kb, lds + now);
-    now ^= kBuffer;
+    multiply(std::false_type{}, std::false_type{}, kb, lds + now, 0, 0);
+    advance();
+  }
+  if (kb < a.kbytes) {
+    wait_copies_and_meet<0>();
+    multiply(std::false_type{}, std::true_type{}, kb, lds + now, 0, 0);
   }
 
   const auto result = [&](int f, int t, float v[4]) {
@@ -342,20 +397,215 @@ __global__ void __launch_bounds__(64 * WT * WC) grouped_kernel(GroupedArgs a) {
   }
 }
 
-template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC>
-hipError_t launch_tile(const GroupedArgs& a, hipStream_t s) {
-  const int chan = kGated ? BC / 2 : BC;
-  const int64_t tiles = a.rows / BT + std::min(a.n_groups, a.rows);
-  const int64_t grid = (tiles * ((a.n + chan - 1) / chan) + 7) / 8 * 8;
+// Few rows per group: the weights stream from memory straight into the
+// registers of the matrix cores, without LDS.  One block: FT x 16 tokens and FC x
+// 16 weight rows (gated: up and gate in turn), whose K is dealt out to KW waves
+// step by step; the waves' sums meet in LDS at the end, added in wave order.
+// While a wave multiplies U steps, the loads of the next U are under way.
+template <typename T, bool kGated, int kOut, int FT, int FC, int KW, int U>
+__global__ void __launch_bounds__(64 * KW) stream_kernel(GroupedArgs a) {
+  constexpr bool kFp8 = std::is_same<T, Fp8Tag>::value;
+  static_assert(!kGated || FC % 2 == 0, "up and gate of a channel belong together");
+  static_assert(FC <= 8, "a block's channels lie in one scale block");
+  __shared__ f32x4_t part[KW][FC * FT][64];
+  __shared__ Item s_item;
+  __shared__ int s_total[KW];
+  constexpr int kChannels = FC * (kGated ? 8 : 16);
+  const int channel_tiles = (a.n + kChannels - 1) / kChannels;
+  if (!find_item(a, FT * 16, channel_tiles, &s_item, s_total)) return;
+  const Item it = {__builtin_amdgcn_readfirstlane(s_item.group), __builtin_amdgcn_readfirstlane(s_item.row0),
+                   __builtin_amdgcn_readfirstlane(s_item.rows), __builtin_amdgcn_readfirstlane(s_item.channel_tile)};
+  const int lane = threadIdx.x & 63, row = lane & 15, quad = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c0 = it.channel_tile * kChannels;
+  const int64_t first = it.group * a.w_group + c0 * a.w_stride;
+  const uint8_t* const w_up = a.w + first;
+  const uint8_t* const w_gate = kGated ? a.w_gate + first : w_up;
+  uint32_t woff[FC];
+#pragma unroll
+  for (int f = 0; f < FC; ++f) {
+    const int j = min((kGated ? f / 2 : f) * 16 + row, a.n - 1 - c0);
+    woff[f] = static_cast<uint32_t>(j) * static_cast<uint32_t>(a.w_stride) + quad * 16;
+  }
+  const auto source = [&](int r) {  // the row of a for row r of the tile, or -1
+    r = it.row0 + min(r, it.rows - 1);
+    const int src = a.row_index ? a.row_index[r] : r;
+    return src < a.a_rows ? src : -1;
+  };
+  const uint8_t* xsrc[FT];
+  const float* xs[FT];
+#pragma unroll
+  for (int t = 0; t < FT; ++t) {
+    const int src = max(source(t * 16 + row), 0);
+    xsrc[t] = a.a + src * a.a_stride + quad * 16;
+    xs[t] = kFp8 ? a.a_scale + static_cast<int64_t>(src) * a.kblocks : nullptr;
+  }
+  const float *wsc_up = nullptr, *wsc_gate = nullptr;
+  if constexpr (kFp8) {
+    const int64_t block = (static_cast<int64_t>(it.group) * a.nblocks + c0 / kScaleBlock) * a.kblocks;
+    wsc_up = a.w_scale + block;
+    wsc_gate = kGated ? a.w_gate_scale + block : wsc_up;
+  }
+  f32x4_t acc[FC][FT];
+#pragma unroll
+  for (int f = 0; f < FC; ++f)
+#pragma unroll
+    for (int t = 0; t < FT; ++t) acc[f][t] = f32x4_t{0, 0, 0, 0};
+
+  struct Step {
+    Frag w[FC], x[FT];
+    float xscale[FT];
+  };
+  const auto load = [&](int step, Step& s) {
+    const int kb = step * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int f = 0; f < FC; ++f)
+        s.w[f].c[h] = *reinterpret_cast<const u32x4_t*>((kGated && (f & 1) ? w_gate : w_up) + kb + woff[f] + h * 64);
+#pragma unroll
+      for (int t = 0; t < FT; ++t) s.x[t].c[h] = *reinterpret_cast<const u32x4_t*>(xsrc[t] + kb + h * 64);
+    }
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int t = 0; t < FT; ++t) s.xscale[t] = xs[t][step];
+    }
+  };
+  const auto multiply = [&](int step, const Step& s) {
+    float ws_up = 0.f, ws_gate = 0.f;
+    if constexpr (kFp8) {
+      ws_up = wsc_up[step];
+      ws_gate = kGated ? wsc_gate[step] : ws_up;
+    }
+#pragma unroll
+    for (int f = 0; f < FC; ++f)
+#pragma unroll
+      for (int t = 0; t < FT; ++t) {
+        if constexpr (kFp8) {
+          const f32x4_t p = mma<T>(s.w[f], s.x[t], f32x4_t{0, 0, 0, 0});
+          const float sc = s.xscale[t] * (kGated && (f & 1) ? ws_gate : ws_up);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(p[i], sc, acc[f][t][i]);
+        } else {
+          acc[f][t] = mma<T>(s.w[f], s.x[t], acc[f][t]);
+        }
+      }
+  };
+  const int whole_steps = a.kbytes >> 7;
+  // this wave's steps: wave, wave + KW, ...; a step past the end repeats the
+  // wave's first one (or step 0) and is not multiplied
+  const int mine = whole_steps > wave ? (whole_steps - wave + KW - 1) / KW : 0;
+  Step buf[2][U];
+  const auto fetch = [&](int i0, Step* b) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(i0 + u < mine ? wave + (i0 + u) * KW : wave, b[u]);
+  };
+  if (mine > 0) {
+    fetch(0, buf[0]);
+    for (int i0 = 0; i0 < mine; i0 += 2 * U) {
+      if (i0 + U < mine) fetch(i0 + U, buf[1]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u < mine) multiply(wave + (i0 + u) * KW, buf[0][u]);
+      if (i0 + U >= mine) break;
+      if (i0 + 2 * U < mine) fetch(i0 + 2 * U, buf[0]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + U + u < mine) multiply(wave + (i0 + U + u) * KW, buf[1][u]);
+    }
+  }
+  if ((a.kbytes & 127) && whole_steps % KW == wave) {  // the part of a step at the end of k
+    Step s;
+    const int kb = whole_steps * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = kb + (h * 4 + quad) * 16 < a.kbytes;
+#pragma unroll
+      for (int f = 0; f < FC; ++f) {
+        const uint8_t* p = (kGated && (f & 1) ? w_gate : w_up) + kb + woff[f] + h * 64;
+        s.w[f].c[h] = *(in ? reinterpret_cast<const u32x4_t*>(p) : &g_zero16);
+      }
+#pragma unroll
+      for (int t = 0; t < FT; ++t)
+        s.x[t].c[h] = *(in ? reinterpret_cast<const u32x4_t*>(xsrc[t] + kb + h * 64) : &g_zero16);
+    }
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int t = 0; t < FT; ++t) s.xscale[t] = xs[t][whole_steps];
+    }
+    multiply(whole_steps, s);
+  }
+#pragma unroll
+  for (int f = 0; f < FC; ++f)
+#pragma unroll
+    for (int t = 0; t < FT; ++t) part[wave][f * FT + t][lane] = acc[f][t];
+  __syncthreads();
+  const bool whole = a.vec_out && c0 + kChannels <= a.n;
+  constexpr int kSums = (kGated ? FC / 2 : FC) * FT;
+  for (int i = wave; i < kSums; i += KW) {
+    const int f = i / FT * (kGated ? 2 : 1), t = i % FT;
+    const int r = t * 16 + row;
+    if (r >= it.rows) continue;
+    f32x4_t u = part[0][f * FT + t][lane], z = f32x4_t{0, 0, 0, 0};
+    for (int w = 1; w < KW; ++w) u += part[w][f * FT + t][lane];
+    if constexpr (kGated) {
+      z = part[0][(f + 1) * FT + t][lane];
+      for (int w = 1; w < KW; ++w) z += part[w][(f + 1) * FT + t][lane];
+    }
+    const bool none = source(r) < 0;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = none ? 0.f : kGated ? u[e] * gate_act(z[e], a.act) : u[e];
+    store4<kOut>(a, whole, static_cast<int64_t>(it.row0) + r, c0 + (kGated ? f / 2 : f) * 16 + quad * 4, v);
+  }
+}
+
+// Blocks of a launch: at least the items that offsets can make.
+int64_t grid_blocks(const GroupedArgs& a, int bt, int channels) {
+  const int64_t tiles = a.rows / bt + std::min(a.n_groups, a.rows);
+  return (tiles * ((a.n + channels - 1) / channels) + 7) / 8 * 8;
+}
+
+template <typename T, bool kGated, int kOut, int FT, int FC, int KW, int U>
+hipError_t launch_stream(const GroupedArgs& a, hipStream_t s) {
+  const int64_t grid = grid_blocks(a, FT * 16, FC * (kGated ? 8 : 16));
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  grouped_kernel<T, kGated, kOut, BT, BC, WT, WC><<<dim3(static_cast<unsigned>(grid)), dim3(64 * WT * WC), 0, s>>>(a);
+  stream_kernel<T, kGated, kOut, FT, FC, KW, U><<<dim3(static_cast<unsigned>(grid)), dim3(64 * KW), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC, int S>
+hipError_t launch_tile(const GroupedArgs& a, hipStream_t s) {
+  const int64_t grid = grid_blocks(a, BT, kGated ? BC / 2 : BC);
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  grouped_kernel<T, kGated, kOut, BT, BC, WT, WC, S><<<dim3(static_cast<unsigned>(grid)), dim3(64 * WT * WC), 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, bool kGated, int kOut>
 hipError_t launch_typed(const GroupedArgs& a, hipStream_t s) {
-  if (a.rows / a.n_groups >= 128) return launch_tile<T, kGated, kOut, 256, 256, 4, 2>(a, s);
-  return launch_tile<T, kGated, kOut, 64, 128, 2, 2>(a, s);
+  const int per_group = (a.rows + a.n_groups - 1) / a.n_groups;
+  constexpr int F1 = kGated ? 2 : 1;
+  const int force = getenv("PX_FORCE") ? atoi(getenv("PX_FORCE")) : 0;
+  int v = force;
+  if (v == 0) v = per_group >= 128 ? 1 : per_group > 32 ? 2 : 6;
+  switch (v) {
+    case 1: return launch_tile<T, kGated, kOut, 256, 256, 4, 2, 2>(a, s);
+    case 2: return launch_tile<T, kGated, kOut, 64, 128, 2, 2, 3>(a, s);
+    case 3: return launch_stream<T, kGated, kOut, 1, F1, 8, 3>(a, s);
+    case 4: return launch_tile<T, kGated, kOut, 64, 128, 2, 2, 4>(a, s);
+    case 5: return launch_stream<T, kGated, kOut, 1, 2, 4, 3>(a, s);
+    case 6: return launch_stream<T, kGated, kOut, 2, 2, 4, 2>(a, s);
+    case 7: return launch_stream<T, kGated, kOut, 2, 4, 4, 1>(a, s);
+    case 8: return launch_tile<T, kGated, kOut, 64, 64, 2, 2, 3>(a, s);
+    case 9: return launch_tile<T, kGated, kOut, 64, 64, 2, 2, 4>(a, s);
+    case 10: return launch_tile<T, kGated, kOut, 128, 128, 2, 2, 2>(a, s);
+    case 11: return launch_tile<T, kGated, kOut, 128, 128, 2, 2, 3>(a, s);
+    case 12: return launch_tile<T, kGated, kOut, 32, 64, 1, 2, 4>(a, s);
+    case 13: return launch_tile<T, kGated, kOut, 128, 256, 2, 4, 3>(a, s);
+    case 14: return launch_tile<T, kGated, kOut, 32, 64, 1, 2, 8>(a, s);
+  }
+  return hipErrorInvalidValue;
 }
 
 template <typename T>
