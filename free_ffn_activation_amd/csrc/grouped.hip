@@ -155,28 +155,43 @@ __device__ __forceinline__ bool find_item(const GroupedArgs& a, int bt, int chan
   return true;
 }
 
-template <int kOut>
-__device__ __forceinline__ void store4(const GroupedArgs& a, bool whole, int64_t row, int j, const float v[4]) {
+__device__ __forceinline__ Item uniform(const Item& i) {
+  return {__builtin_amdgcn_readfirstlane(i.group), __builtin_amdgcn_readfirstlane(i.row0),
+          __builtin_amdgcn_readfirstlane(i.rows), __builtin_amdgcn_readfirstlane(i.channel_tile)};
+}
+
+// kCount neighbouring results from channel j on into the row of out at q; `left`
+// of them exist; vec: rows of out are 16-byte aligned (j is a multiple of kCount).
+template <int kOut, int kCount>
+__device__ __forceinline__ void store_results(uint8_t* q, int j, const float (&v)[kCount], int left, bool vec) {
   if constexpr (kOut == PROX_F32) {
-    float* p = reinterpret_cast<float*>(a.out + row * a.out_stride) + j;
-    if (whole) {
-      *reinterpret_cast<f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
+    float* p = reinterpret_cast<float*>(q) + j;
+    if (vec && left >= kCount) {
+#pragma unroll
+      for (int h = 0; h < kCount; h += 4)
+        *reinterpret_cast<f32x4_t*>(p + h) = f32x4_t{v[h], v[h + 1], v[h + 2], v[h + 3]};
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (j + i < a.n) p[i] = v[i];
+      for (int i = 0; i < kCount; ++i)
+        if (i < left) p[i] = v[i];
     }
   } else {
-    __bf16* p = reinterpret_cast<__bf16*>(a.out + row * a.out_stride) + j;
-    if (whole) {
-      *reinterpret_cast<bf16x4_t*>(p) = bf16x4_t{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    typedef __attribute__((ext_vector_type(kCount))) __bf16 vec_t;
+    __bf16* p = reinterpret_cast<__bf16*>(q) + j;
+    vec_t b;
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) b[i] = (__bf16)v[i];
+    if (vec && left >= kCount) {
+      *reinterpret_cast<vec_t*>(p) = b;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (j + i < a.n) p[i] = (__bf16)v[i];
+      for (int i = 0; i < kCount; ++i)
+        if (i < left) p[i] = b[i];
     }
   }
 }
+
+constexpr uint32_t kWidePart = 32 * (8 * 16 + 4) * 4;  // wide kernel: LDS of a wave's results, two token fragments
 
 // Waits until at most kLeft of this wave's memory-to-LDS copies are under way,
 // and for its LDS reads, then for the other waves of the block.
@@ -185,71 +200,183 @@ __device__ __forceinline__ void wait_copies_and_meet() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
 }
 
+// The row of a for row r of the tile (rows past the tile's last repeat it), or
+// -1 for a row index outside a.
+__device__ __forceinline__ int source_row(const GroupedArgs& a, const Item& it, int r) {
+  r = it.row0 + min(r, it.rows - 1);
+  const int src = a.row_index ? a.row_index[r] : r;
+  return src < a.a_rows ? src : -1;
+}
+
+// One lane's share of the copies that bring a step of a tile (BT tokens, BC weight
+// rows, 128 bytes of k) into LDS: weight rows first, then tokens, then (fp8)
+// scales.  A copy of a wave is eight rows; lane l brings the chunk at place l % 8
+// of row l / 8.  Rows past the last token or channel of the tile repeat a row that
+// exists; their results are not stored.
+template <bool kGated, bool kFp8, int BT, int BC, int kWaves>
+struct TileCopies {
+  static constexpr int NW = BC / 8 / kWaves, NX = BT / 8 / kWaves, kCount = NW + NX + (kFp8 ? 1 : 0);
+  static constexpr uint32_t kScales = (BC + BT) * 128;  // their place in a buffer
+  static constexpr uint32_t kBuffer = kScales + (kFp8 ? kWaves * 256 : 0);
+  // fp8: wave i < kTokenWaves brings the scales of 64 tokens, the next wave those
+  // of the channels (kBlocks blocks of 128, up then gate); lanes and waves
+  // without a scale repeat another
+  static constexpr int kTokenWaves = (BT + 63) / 64, kBlocks = BC / (kGated ? 256 : 128) + 1;
+  static_assert(NW * 8 * kWaves == BC && NX * 8 * kWaves == BT, "whole copies");
+  static_assert(!kFp8 || kTokenWaves < kWaves, "a wave is left for the channels' scales");
+
+  // uniform: the tile's first channel in the matrix that copy i takes rows of, for
+  // even and odd i (sixteens of rows are up and gate in turn, so with four or more
+  // waves all copies of a wave take the same one)
+  const uint8_t *w_even, *w_odd;
+  uint32_t woff[NW];             // below 2^31: at most 256 rows of less than 2^23 bytes
+  const uint8_t* xsrc[NX];
+  const float* scale;
+  int kbytes, chunk, wave;
+
+  __device__ __forceinline__ void init(const GroupedArgs& a, const Item& it, int c0, int wave_, int lane) {
+    const int crow = lane >> 3;
+    chunk = ((lane & 7) ^ crow) * 16;
+    wave = wave_;
+    kbytes = a.kbytes;
+    const int64_t first = it.group * a.w_group + c0 * a.w_stride;
+    const uint8_t* const up = a.w + first;
+    const uint8_t* const gate = kGated ? a.w_gate + first : up;
+    static_assert(kWaves == 2 || kWaves % 4 == 0, "copies take up or gate rows by wave, or in turn");
+    w_even = kWaves > 2 && (wave >> 1 & 1) ? gate : up;
+    w_odd = kWaves > 2 ? w_even : gate;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int r = (i * kWaves + wave) * 8 + crow;
+      const int j = min(kGated ? (r >> 5) * 16 + (r & 15) : r, a.n - 1 - c0);
+      woff[i] = static_cast<uint32_t>(j) * static_cast<uint32_t>(a.w_stride) + chunk;
+    }
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+      xsrc[i] = a.a + max(source_row(a, it, (i * kWaves + wave) * 8 + crow), 0) * a.a_stride + chunk;
+    scale = nullptr;
+    if constexpr (kFp8) {
+      if (wave < kTokenWaves) {
+        scale = a.a_scale + static_cast<int64_t>(max(source_row(a, it, wave * 64 + lane), 0)) * a.kblocks;
+      } else {
+        const int block = min(c0 / kScaleBlock + lane % kBlocks, a.nblocks - 1);
+        scale = (kGated && (lane / kBlocks & 1) ? a.w_gate_scale : a.w_scale) +
+                (static_cast<int64_t>(it.group) * a.nblocks + block) * a.kblocks;
+      }
+    }
+  }
+
+  // This lane's offset for the step at byte kb.  Chunks past the end of k (in the
+  // last step only) repeat the step's first one; the products take zeros there.
+  __device__ __forceinline__ int offset(int kb) const { return kb + chunk < kbytes ? kb : kb - chunk; }
+
+  // Copy i of the step at kb (off: offset(kb)) into the buffer at LDS byte `to`.
+  __device__ __forceinline__ void go(int i, int kb, int off, uint32_t to) const {
+    if (i < NW) {
+      copy16((i & 1) ? w_odd : w_even, woff[i] + off, to + (i * kWaves + wave) * 1024);
+    } else if (i < NW + NX) {
+      copy16(xsrc[i - NW] + off, to + BC * 128 + ((i - NW) * kWaves + wave) * 1024);
+    } else if constexpr (kFp8) {
+      copy4(scale + (kb >> 7), to + kScales + wave * 256);
+    }
+  }
+};
+
+// The two 16-byte chunks of this lane's row in a fragment at p.
+struct Places {
+  int row, quad, place[2];
+  __device__ __forceinline__ explicit Places(int lane)
+      : row(lane & 15), quad(lane >> 4), place{((lane >> 4) ^ (lane & 7)) << 4, ((4 + (lane >> 4)) ^ (lane & 7)) << 4} {}
+  __device__ __forceinline__ Frag read(const uint8_t* p) const {
+    Frag r;
+    r.c[0] = *reinterpret_cast<const u32x4_t*>(p + place[0]);
+    r.c[1] = *reinterpret_cast<const u32x4_t*>(p + place[1]);
+    return r;
+  }
+};
+
+// The wave's results, FC x 16 weight rows by FT x 16 tokens, to out.  They go
+// through the wave's own part of LDS, TP token fragments at a time, so that a row
+// of out is written in whole lines and the activation is one short loop (held in
+// registers it is unrolled to 40 KB of code, which every CU first has to fetch).
+// first: the wave's first channel; token_row(t): the tile's row of fragment t.
+template <bool kGated, int kOut, int FC, int FT, int TP, typename Rows>
+__device__ __forceinline__ void write_results(const GroupedArgs& a, const Item& it, const f32x4_t (&acc)[FC][FT],
+                                              float* part, int lane, int first, Rows token_row) {
+  constexpr int kStride = FC * 16 + 4;                 // floats per token: rows four banks apart
+  constexpr int kChannels = FC * (kGated ? 8 : 16);    // results per token
+  constexpr int kLanes = kChannels / 8, kPer = 64 / kLanes;  // lanes of a token, tokens at a time
+  const int row = lane & 15, quad = lane >> 4;
+  const int slot = lane / kLanes, j0 = lane % kLanes * 8;
+  const int left = a.n - first - j0;  // results that exist from this lane's first on
+#pragma unroll
+  for (int t0 = 0; t0 < FT; t0 += TP) {
+#pragma unroll
+    for (int t = t0; t < t0 + TP; ++t)
+#pragma unroll
+      for (int f = 0; f < FC; ++f)
+        *reinterpret_cast<f32x4_t*>(part + ((t - t0) * 16 + row) * kStride + f * 16 + quad * 4) = acc[f][t];
+#pragma unroll 1
+    for (int i = slot; i < TP * 16; i += kPer) {
+      const int r = token_row(t0 + (i >> 4)) + (i & 15);
+      if (r >= it.rows || left <= 0) continue;
+      // a channel's up and gate are sixteen rows apart
+      const float* p = part + i * kStride + (kGated ? (j0 >> 4) * 32 + (j0 & 15) : j0);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = p[e];
+      if constexpr (kGated) {
+        if (a.act == PROX_ACT_SILU) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= silu_f32(p[16 + e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= gelu_tanh_f32(p[16 + e]);
+        }
+      }
+      if (a.row_index && source_row(a, it, r) < 0) {  // a row index outside a: zeros
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      }
+      uint8_t* q = a.out + (static_cast<int64_t>(it.row0) + r) * a.out_stride;
+      store_results<kOut, 8>(q, first + j0, v, left, a.vec_out);
+    }
+  }
+}
+
 // One block: BT tokens x BC weight rows (gated: BC / 2 channels, up and gate in
 // turn by sixteen rows), WC x WT waves, S LDS buffers: while the waves multiply
 // step s, the copies of steps s + 1 .. s + S - 1 are under way.
 template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC, int S>
-__global__ void __launch_bounds__(64 * WT * WC) grouped_kernel(GroupedArgs a) {
+__global__ void __launch_bounds__(64 * WT * WC) tile_kernel(GroupedArgs a) {
   constexpr int kWaves = WT * WC, FC = BC / 16 / WC, FT = BT / 16 / WT;  // fragments of 16 per wave
-  constexpr int NW = BC / 8 / kWaves, NX = BT / 8 / kWaves;              // copies per wave and step
   constexpr bool kFp8 = std::is_same<T, Fp8Tag>::value;
-  constexpr uint32_t kBuffer = (BC + BT) * 128 + (kFp8 ? kWaves * 256 : 0);
-  constexpr int kCopies = NW + NX + (kFp8 ? 1 : 0);
-  static_assert(NW * 8 * kWaves == BC && NX * 8 * kWaves == BT && FC * 16 * WC == BC && FT * 16 * WT == BT, "tile");
+  typedef TileCopies<kGated, kFp8, BT, BC, kWaves> Copies;
+  static_assert(FC * 16 * WC == BC && FT * 16 * WT == BT, "tile");
   static_assert(FC <= 8 && 128 % (FC * 16) == 0, "a wave's channels lie in one scale block");
   static_assert(!kGated || FC % 2 == 0, "up and gate of a channel belong to one wave");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[S * kBuffer];
+  constexpr uint32_t kBuffer = Copies::kBuffer, kCopies = Copies::kCount;
+  constexpr int TP = FT < 2 ? FT : 2;                       // token fragments written at a time
+  constexpr uint32_t kPart = TP * 16 * (FC * 16 + 4) * 4;  // LDS of a wave's results
+  constexpr uint32_t kLds = S * kBuffer > kWaves * kPart ? S * kBuffer : kWaves * kPart;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   __shared__ Item s_item;
   __shared__ int s_total[kWaves];
   const int chan_per_tile = kGated ? BC / 2 : BC;
   const int channel_tiles = (a.n + chan_per_tile - 1) / chan_per_tile;
   if (!find_item(a, BT, channel_tiles, &s_item, s_total)) return;
-  const Item it = {__builtin_amdgcn_readfirstlane(s_item.group), __builtin_amdgcn_readfirstlane(s_item.row0),
-                   __builtin_amdgcn_readfirstlane(s_item.rows), __builtin_amdgcn_readfirstlane(s_item.channel_tile)};
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Item it = uniform(s_item);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wc = wave / WT, wt = wave % WT;  // this wave's share of the channels and of the tokens
   const int c0 = it.channel_tile * chan_per_tile;
-
-  // Rows that this lane copies: eight rows per wave and copy, lane l the chunk
-  // at place l % 8 of row l / 8.  Rows past the last token or channel of the
-  // tile repeat a row that exists; their results are not stored.
-  const int crow = lane >> 3, chunk = (lane & 7) ^ crow;
-  // uniform: the tile's first channel, up and gate
-  const int64_t first = it.group * a.w_group + c0 * a.w_stride;
-  const uint8_t* const w_up = a.w + first;
-  const uint8_t* const w_gate = kGated ? a.w_gate + first : w_up;
-  uint32_t woff[NW];  // below 2^31: at most 256 rows of less than 2^23 bytes
-  const uint8_t* xsrc[NX];
-#pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    const int r = (i * kWaves + wave) * 8 + crow;
-    const int j = min(kGated ? (r >> 5) * 16 + (r & 15) : r, a.n - 1 - c0);
-    woff[i] = static_cast<uint32_t>(j) * static_cast<uint32_t>(a.w_stride) + chunk * 16;
-  }
-  const auto source = [&](int r) {  // the row of a for row r of the tile, or -1
-    r = it.row0 + min(r, it.rows - 1);
-    const int src = a.row_index ? a.row_index[r] : r;
-    return src < a.a_rows ? src : -1;
-  };
-#pragma unroll
-  for (int i = 0; i < NX; ++i)
-    xsrc[i] = a.a + max(source((i * kWaves + wave) * 8 + crow), 0) * a.a_stride + chunk * 16;
-  // fp8: each step brings the scales of the tile's tokens (64 a wave) and of its
-  // channels (the wave after those: lane l the l-th block of 128, up then gate)
-  // into LDS by one copy per wave, whose lanes without a scale repeat another
-  constexpr int kTokenWaves = (BT + 63) / 64, kBlocks = BC / (kGated ? 256 : 128) + 1;
-  static_assert(!kFp8 || kTokenWaves < kWaves, "a wave is left for the channels' scales");
-  const float* scale_src = nullptr;
-  if constexpr (kFp8) {
-    if (wave < kTokenWaves) {
-      scale_src = a.a_scale + static_cast<int64_t>(max(source(wave * 64 + lane), 0)) * a.kblocks;
-    } else {
-      const int block = min(c0 / kScaleBlock + lane % kBlocks, a.nblocks - 1);
-      scale_src = (kGated && (lane / kBlocks & 1) ? a.w_gate_scale : a.w_scale) +
-                  (static_cast<int64_t>(it.group) * a.nblocks + block) * a.kblocks;
-    }
-  }
+  const int first = c0 + wc * FC * (kGated ? 8 : 16);
+  Copies copies;
+  copies.init(a, it, c0, wave, lane);
+  const Places at(lane);
+  const uint32_t lds0 = lds_offset(lds);
+  // the block of 128 channels that this wave's lie in, from the tile's first on
+  const int block = first / kScaleBlock - c0 / kScaleBlock;
 
   f32x4_t acc[FC][FT];
 #pragma unroll
@@ -257,38 +384,16 @@ __global__ void __launch_bounds__(64 * WT * WC) grouped_kernel(GroupedArgs a) {
 #pragma unroll
     for (int t = 0; t < FT; ++t) acc[f][t] = f32x4_t{0, 0, 0, 0};
 
-  constexpr uint32_t kScales = (BC + BT) * 128;  // their place in a buffer
-  const uint32_t lds0 = lds_offset(lds);
-  // copy i of the step at byte kb of the rows.  Chunks past the end of k (in the
-  // last step only) repeat the step's first one; multiply() takes zeros there.
-  const auto copy = [&](int i, int kb, int lane_kb, uint32_t to) {
-    to += lds0 + wave * 1024;
-    if (i < NW) {  // up (even sixteens of rows) or gate
-      copy16((kGated && (((i * kWaves + wave) >> 1) & 1) ? w_gate : w_up), woff[i] + lane_kb,
-             to + i * (kWaves * 1024));
-    } else if (i < NW + NX) {
-      copy16(xsrc[i - NW] + lane_kb, to + BC * 128 + (i - NW) * (kWaves * 1024));
-    } else if constexpr (kFp8) {
-      copy4(scale_src + (kb >> 7), to - wave * 768 + kScales);
-    }
-  };
-  const auto lane_offset = [&](int kb) { return kb + chunk * 16 < a.kbytes ? kb : kb - chunk * 16; };
-  const int row = lane & 15, quad = lane >> 4;
-  const int place0 = ((quad) ^ (row & 7)) << 4, place1 = ((4 + quad) ^ (row & 7)) << 4;
-  // the block of 128 channels that this wave's lie in, from the tile's first on
-  const int block = (c0 + wc * FC * (kGated ? 8 : 16)) / kScaleBlock - c0 / kScaleBlock;
-  // Multiplies the step in `from`, and meanwhile (more) issues the copies of the
-  // step at next_kb into `to`, a few between the products.
-  const auto multiply = [&](auto more, auto tail, int kb, const uint8_t* from, int next_kb, uint32_t to) {
-    const uint8_t* pw = from + (wc * FC * 16 + row) * 128;
-    const uint8_t* px = from + BC * 128 + (wt * FT * 16 + row) * 128;
+  // Multiplies the step in buffer `from`, and meanwhile (more) issues the copies
+  // of the step at next_kb into `to`, a few between the products.
+  const auto multiply = [&](auto more, auto last, int kb, uint32_t from, int next_kb, uint32_t to) {
+    const uint8_t* pw = lds + from + (wc * FC * 16 + at.row) * 128;
+    const uint8_t* px = lds + from + BC * 128 + (wt * FT * 16 + at.row) * 128;
     const auto read = [&](const uint8_t* p) {
-      Frag r;
-      r.c[0] = *reinterpret_cast<const u32x4_t*>(p + place0);
-      r.c[1] = *reinterpret_cast<const u32x4_t*>(p + place1);
-      if constexpr (decltype(tail)::value) {
-        if (kb + quad * 16 >= a.kbytes) r.c[0] = u32x4_t{0, 0, 0, 0};
-        if (kb + quad * 16 + 64 >= a.kbytes) r.c[1] = u32x4_t{0, 0, 0, 0};
+      Frag r = at.read(p);
+      if constexpr (decltype(last)::value) {  // chunks past the end of k count as zeros
+        if (kb + at.quad * 16 >= a.kbytes) r.c[0] = u32x4_t{0, 0, 0, 0};
+        if (kb + at.quad * 16 + 64 >= a.kbytes) r.c[1] = u32x4_t{0, 0, 0, 0};
       }
       return r;
     };
@@ -297,13 +402,13 @@ __global__ void __launch_bounds__(64 * WT * WC) grouped_kernel(GroupedArgs a) {
 #pragma unroll
     for (int t = 0; t < FT; ++t) xf[t] = read(px + t * 2048);
     float xscale[FT], ws_up = 0.f, ws_gate = 0.f;
-    f32x4_t part[2][FT];  // fp8: a step's products, scaled and added one fragment later
+    f32x4_t part[2][FT];  // fp8: a fragment's products, scaled and added one fragment later
     if constexpr (kFp8) {
-      const float* ps = reinterpret_cast<const float*>(from + kScales);
+      const float* ps = reinterpret_cast<const float*>(lds + from + Copies::kScales);
 #pragma unroll
-      for (int t = 0; t < FT; ++t) xscale[t] = ps[(wt * FT + t) * 16 + row];
-      ws_up = ps[kTokenWaves * 64 + block];
-      ws_gate = kGated ? ps[kTokenWaves * 64 + kBlocks + block] : ws_up;
+      for (int t = 0; t < FT; ++t) xscale[t] = ps[(wt * FT + t) * 16 + at.row];
+      ws_up = ps[Copies::kTokenWaves * 64 + block];
+      ws_gate = kGated ? ps[Copies::kTokenWaves * 64 + Copies::kBlocks + block] : ws_up;
     }
     const auto add = [&](int f) {
 #pragma unroll
@@ -313,14 +418,14 @@ __global__ void __launch_bounds__(64 * WT * WC) grouped_kernel(GroupedArgs a) {
         for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(part[f & 1][t][i], sc, acc[f][t][i]);
       }
     };
-    const int lane_kb = lane_offset(next_kb);
+    const int off = copies.offset(next_kb);
 #pragma unroll
     for (int f = 0; f < FC; ++f) {
       // the next channels' fragment is read while this one is multiplied
       if (f + 1 < FC) wf[(f + 1) & 1] = read(pw + (f + 1) * 2048);
       if constexpr (decltype(more)::value) {
 #pragma unroll
-        for (int i = f * kCopies / FC; i < (f + 1) * kCopies / FC; ++i) copy(i, next_kb, lane_kb, to);
+        for (int i = f * kCopies / FC; i < (f + 1) * kCopies / FC; ++i) copies.go(i, next_kb, off, lds0 + to);
       }
 #pragma unroll
       for (int t = 0; t < FT; ++t) {
@@ -346,9 +451,9 @@ __global__ void __launch_bounds__(64 * WT * WC) grouped_kernel(GroupedArgs a) {
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) {
     if (i * 128 < a.kbytes) {
-      const int lane_kb = lane_offset(i * 128);
+      const int off = copies.offset(i * 128);
 #pragma unroll
-      for (int c = 0; c < kCopies; ++c) copy(c, i * 128, lane_kb, next);
+      for (int c = 0; c < static_cast<int>(kCopies); ++c) copies.go(c, i * 128, off, lds0 + next);
     }
     next += kBuffer;
   }
@@ -360,41 +465,190 @@ __global__ void __launch_bounds__(64 * WT * WC) grouped_kernel(GroupedArgs a) {
   for (; kb + (S - 1) * 128 < a.kbytes; kb += 128) {
     // this step's copies are done when only those of the later steps are left
     wait_copies_and_meet<(S - 2) * kCopies>();
-    multiply(std::true_type{}, std::false_type{}, kb, lds + now, kb + (S - 1) * 128, next);
+    multiply(std::true_type{}, std::false_type{}, kb, now, kb + (S - 1) * 128, next);
     advance();
   }
-  for (; kb + 128 <= a.kbytes; kb += 128) {
+  for (; kb + 128 < a.kbytes; kb += 128) {
     wait_copies_and_meet<0>();
-    multiply(std::false_type{}, std::false_type{}, kb, lds + now, 0, 0);
+    multiply(std::false_type{}, std::false_type{}, kb, now, 0, 0);
     advance();
   }
-  if (kb < a.kbytes) {
-    wait_copies_and_meet<0>();
-    multiply(std::false_type{}, std::true_type{}, kb, lds + now, 0, 0);
-  }
+  wait_copies_and_meet<0>();
+  multiply(std::false_type{}, std::true_type{}, kb, now, 0, 0);
+  wait_copies_and_meet<0>();  // every wave has read its last step
+  write_results<kGated, kOut, FC, FT, TP>(a, it, acc, reinterpret_cast<float*>(lds + wave * kPart), lane, first,
+                                          [&](int t) { return (wt * FT + t) * 16; });
+}
 
-  const auto result = [&](int f, int t, float v[4]) {
+// Many rows per group: one block computes 256 tokens x 256 weight rows (gated:
+// 128 channels, up and gate in turn by sixteen rows) with eight waves of 64
+// tokens x 128 weight rows, from two LDS buffers of one step each.  A step has two
+// meeting points of the waves: at the first, the tokens and the lower half of
+// every wave's channels have been read, at the second the upper half; each part
+// is overwritten with the copies of the step after next as soon as it is free.
+// So a copy has one and a half steps to arrive, and a wait leaves a whole step's
+// copies under way (one meeting per step and one step of distance: 5 to 10 %
+// slower).  After the second meeting the first fragments of the next step are read
+// under the last products of this one.
+// The waves take the token fragments in turn, so that a tile of at most 128
+// tokens (FT = 2) costs every wave half the products.
+template <typename T, bool kGated, int kOut, int FT>
+__device__ __forceinline__ void wide_tile(const GroupedArgs& a, const Item& it, uint8_t* lds, int c0) {
+  constexpr int BT = FT * 64, BC = 256, WT = 4, kWaves = 8, FC = 8;
+  constexpr bool kFp8 = std::is_same<T, Fp8Tag>::value;
+  typedef TileCopies<kGated, kFp8, BT, BC, kWaves> Copies;
+  constexpr uint32_t kBuffer = Copies::kBuffer;
+  constexpr int kCopies = Copies::kCount, NW = Copies::NW;
+  static_assert(NW == 4, "copies 0 and 2 of the channels are the lower halves");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wc = wave / WT, wt = wave % WT;  // this wave's share of the channels and of the tokens
+  const int first = c0 + wc * FC * (kGated ? 8 : 16);
+  Copies copies;
+  copies.init(a, it, c0, wave, lane);
+  const Places at(lane);
+  const uint32_t lds0 = lds_offset(lds);
+  const int block = first / kScaleBlock - c0 / kScaleBlock;  // this wave's block of 128 channels in the tile
+
+  f32x4_t acc[FC][FT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = kGated ? acc[f][t][i] * gate_act(acc[f + (kGated ? 1 : 0)][t][i], a.act) : acc[f][t][i];
+  for (int f = 0; f < FC; ++f)
+#pragma unroll
+    for (int t = 0; t < FT; ++t) acc[f][t] = f32x4_t{0, 0, 0, 0};
+
+  const uint8_t* const pw = lds + (wc * FC * 16 + at.row) * 128;
+  const uint8_t* const px = lds + BC * 128 + (wt * 16 + at.row) * 128;
+  Frag xf[FT], wf[2];  // at the start of a step: its tokens and its first channels
+  // Multiplies the step in buffer `from` (the next one is in `then`); more: the
+  // step after that one is copied into `from`.
+  const auto multiply = [&](auto more, auto last, int kb, uint32_t from, uint32_t then) {
+    constexpr bool kMore = decltype(more)::value, kLast = decltype(last)::value;
+    const bool out0 = kb + at.quad * 16 >= a.kbytes, out1 = kb + at.quad * 16 + 64 >= a.kbytes;
+    const auto cut = [&](Frag& r) {  // chunks past the end of k count as zeros
+      if constexpr (kLast) {
+        if (out0) r.c[0] = u32x4_t{0, 0, 0, 0};
+        if (out1) r.c[1] = u32x4_t{0, 0, 0, 0};
+      }
+    };
+    cut(wf[0]);
+#pragma unroll
+    for (int t = 0; t < FT; ++t) cut(xf[t]);
+    float xscale[FT], ws_up = 0.f, ws_gate = 0.f;
+    f32x4_t part[4];  // fp8: products, scaled and added three matrix instructions later
+    if constexpr (kFp8) {
+      const float* ps = reinterpret_cast<const float*>(lds + from + Copies::kScales);
+#pragma unroll
+      for (int t = 0; t < FT; ++t) xscale[t] = ps[(t * WT + wt) * 16 + at.row];
+      ws_up = ps[Copies::kTokenWaves * 64 + block];
+      ws_gate = kGated ? ps[Copies::kTokenWaves * 64 + Copies::kBlocks + block] : ws_up;
+    }
+    const auto add = [&](int n) {  // the n-th instruction's
+      const int f = n / FT, t = n % FT;
+      const float sc = xscale[t] * (kGated && (f & 1) ? ws_gate : ws_up);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(part[n & 3][i], sc, acc[f][t][i]);
+    };
+    const int next_kb = kb + 256, off = kMore ? copies.offset(next_kb) : 0;
+#pragma unroll
+    for (int f = 0; f < FC; ++f) {
+      if (f == FC / 2 - 1) {  // this step's upper half has come; its tokens and lower half are read
+        wait_copies_and_meet<kLast ? 0 : kCopies>();
+      } else if (f == FC - 1 && !kLast) {  // the next step's lower part has come; the upper half is read
+        wait_copies_and_meet<kMore ? kCopies : 2>();
+      }
+      // the next channels' fragment is read while this one is multiplied
+      if (f + 1 < FC) {
+        wf[(f + 1) & 1] = at.read(pw + from + (f + 1) * 2048);
+        cut(wf[(f + 1) & 1]);
+      } else if constexpr (!kLast) {
+        wf[0] = at.read(pw + then);
+      }
+      if constexpr (kMore) {
+        // lower part: spread over three fragments' products (issued at once the
+        // copies hold up the reads); upper half
+        if (f == FC / 2 - 1) {
+          copies.go(0, next_kb, off, lds0 + from);
+          copies.go(2, next_kb, off, lds0 + from);
+        } else if (f == FC / 2 || f == FC / 2 + 1) {
+#pragma unroll
+          for (int i = NW; i < kCopies; ++i)
+            if ((i - NW >= 2) == (f > FC / 2)) copies.go(i, next_kb, off, lds0 + from);
+        } else if (f == FC - 1) {
+          copies.go(1, next_kb, off, lds0 + from);
+          copies.go(3, next_kb, off, lds0 + from);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < FT; ++t) {
+        if constexpr (kFp8) {
+          const int n = f * FT + t;
+          part[n & 3] = mma<T>(wf[f & 1], xf[t], f32x4_t{0, 0, 0, 0});
+          if (n >= 3) add(n - 3);
+          // a matrix instruction, then the sums that fit beside it
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+        } else {
+          acc[f][t] = mma<T>(wf[f & 1], xf[t], acc[f][t]);
+        }
+        if constexpr (!kLast) {
+          if (f == FC - 1) xf[t] = at.read(px + then + t * (WT * 2048));
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int n = FC * FT - 3; n < FC * FT; ++n) add(n);
+    }
   };
-  const bool whole = a.vec_out && c0 + chan_per_tile <= a.n;  // uniform
+  // the first two steps, in the order of the waits: lower parts, then upper halves
 #pragma unroll
-  for (int t = 0; t < FT; ++t) {
-    const int r = (wt * FT + t) * 16 + (lane & 15);
-    if (r >= it.rows) continue;
-    const bool none = source(r) < 0;  // a row index outside a: zeros
+  for (int s = 0; s < 2; ++s) {
+    if (s * 128 < a.kbytes) {
+      const int off = copies.offset(s * 128);
+      const uint32_t to = lds0 + s * kBuffer;
+      copies.go(0, s * 128, off, to);
+      copies.go(2, s * 128, off, to);
 #pragma unroll
-    for (int f = 0; f < FC; f += kGated ? 2 : 1) {
-      const int frag = wc * FC + f;
-      const int j = (kGated ? c0 + (frag >> 1) * 16 : c0 + frag * 16) + quad * 4;
-      float v[4];
-      result(f, t, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = none ? 0.f : v[i];
-      store4<kOut>(a, whole, static_cast<int64_t>(it.row0) + r, j, v);
+      for (int i = NW; i < kCopies; ++i) copies.go(i, s * 128, off, to);
+      copies.go(1, s * 128, off, to);
+      copies.go(3, s * 128, off, to);
     }
   }
+  if (128 < a.kbytes) wait_copies_and_meet<kCopies + 2>();
+  else wait_copies_and_meet<2>();
+  wf[0] = at.read(pw);
+#pragma unroll
+  for (int t = 0; t < FT; ++t) xf[t] = at.read(px + t * (WT * 2048));
+  uint32_t now = 0;  // this step's buffer
+  int kb = 0;
+  for (; kb + 256 < a.kbytes; kb += 128) {
+    multiply(std::true_type{}, std::false_type{}, kb, now, now ^ kBuffer);
+    now ^= kBuffer;
+  }
+  if (kb + 128 < a.kbytes) {
+    multiply(std::false_type{}, std::false_type{}, kb, now, now ^ kBuffer);
+    kb += 128;
+    now ^= kBuffer;
+  }
+  multiply(std::false_type{}, std::true_type{}, kb, now, 0);
+  wait_copies_and_meet<0>();  // every wave has read its last step
+  write_results<kGated, kOut, FC, FT, 2>(a, it, acc, reinterpret_cast<float*>(lds + wave * kWidePart), lane, first,
+                                         [&](int t) { return (t * WT + wt) * 16; });
+}
+
+template <typename T, bool kGated, int kOut>
+__global__ void __launch_bounds__(512) wide_kernel(GroupedArgs a) {
+  constexpr uint32_t kBuffers = 2 * TileCopies<kGated, std::is_same<T, Fp8Tag>::value, 256, 256, 8>::kBuffer;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kBuffers > 8 * kWidePart ? kBuffers : 8 * kWidePart];
+  __shared__ Item s_item;
+  __shared__ int s_total[8];
+  const int chan_per_tile = kGated ? 128 : 256;
+  const int channel_tiles = (a.n + chan_per_tile - 1) / chan_per_tile;
+  if (!find_item(a, 256, channel_tiles, &s_item, s_total)) return;
+  const Item it = uniform(s_item);
+  if (it.rows > 128) wide_tile<T, kGated, kOut, 4>(a, it, lds, it.channel_tile * chan_per_tile);
+  else wide_tile<T, kGated, kOut, 2>(a, it, lds, it.channel_tile * chan_per_tile);
 }
 
 // Few rows per group: the weights stream from memory straight into the
@@ -413,8 +667,7 @@ __global__ void __launch_bounds__(64 * KW) stream_kernel(GroupedArgs a) {
   constexpr int kChannels = FC * (kGated ? 8 : 16);
   const int channel_tiles = (a.n + kChannels - 1) / kChannels;
   if (!find_item(a, FT * 16, channel_tiles, &s_item, s_total)) return;
-  const Item it = {__builtin_amdgcn_readfirstlane(s_item.group), __builtin_amdgcn_readfirstlane(s_item.row0),
-                   __builtin_amdgcn_readfirstlane(s_item.rows), __builtin_amdgcn_readfirstlane(s_item.channel_tile)};
+  const Item it = uniform(s_item);
   const int lane = threadIdx.x & 63, row = lane & 15, quad = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c0 = it.channel_tile * kChannels;
@@ -427,16 +680,11 @@ __global__ void __launch_bounds__(64 * KW) stream_kernel(GroupedArgs a) {
     const int j = min((kGated ? f / 2 : f) * 16 + row, a.n - 1 - c0);
     woff[f] = static_cast<uint32_t>(j) * static_cast<uint32_t>(a.w_stride) + quad * 16;
   }
-  const auto source = [&](int r) {  // the row of a for row r of the tile, or -1
-    r = it.row0 + min(r, it.rows - 1);
-    const int src = a.row_index ? a.row_index[r] : r;
-    return src < a.a_rows ? src : -1;
-  };
   const uint8_t* xsrc[FT];
   const float* xs[FT];
 #pragma unroll
   for (int t = 0; t < FT; ++t) {
-    const int src = max(source(t * 16 + row), 0);
+    const int src = max(source_row(a, it, t * 16 + row), 0);
     xsrc[t] = a.a + src * a.a_stride + quad * 16;
     xs[t] = kFp8 ? a.a_scale + static_cast<int64_t>(src) * a.kblocks : nullptr;
   }
@@ -540,7 +788,6 @@ __global__ void __launch_bounds__(64 * KW) stream_kernel(GroupedArgs a) {
 #pragma unroll
     for (int t = 0; t < FT; ++t) part[wave][f * FT + t][lane] = acc[f][t];
   __syncthreads();
-  const bool whole = a.vec_out && c0 + kChannels <= a.n;
   constexpr int kSums = (kGated ? FC / 2 : FC) * FT;
   for (int i = wave; i < kSums; i += KW) {
     const int f = i / FT * (kGated ? 2 : 1), t = i % FT;
@@ -552,11 +799,12 @@ __global__ void __launch_bounds__(64 * KW) stream_kernel(GroupedArgs a) {
       z = part[0][(f + 1) * FT + t][lane];
       for (int w = 1; w < KW; ++w) z += part[w][(f + 1) * FT + t][lane];
     }
-    const bool none = source(r) < 0;
+    const bool none = source_row(a, it, r) < 0;
     float v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = none ? 0.f : kGated ? u[e] * gate_act(z[e], a.act) : u[e];
-    store4<kOut>(a, whole, static_cast<int64_t>(it.row0) + r, c0 + (kGated ? f / 2 : f) * 16 + quad * 4, v);
+    const int j = c0 + (kGated ? f / 2 : f) * 16 + quad * 4;
+    store_results<kOut, 4>(a.out + (static_cast<int64_t>(it.row0) + r) * a.out_stride, j, v, a.n - j, a.vec_out);
   }
 }
 
@@ -574,11 +822,19 @@ hipError_t launch_stream(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T, bool kGated, int kOut>
+hipError_t launch_wide(const GroupedArgs& a, hipStream_t s) {
+  const int64_t grid = grid_blocks(a, 256, kGated ? 128 : 256);
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  wide_kernel<T, kGated, kOut><<<dim3(static_cast<unsigned>(grid)), dim3(512), 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC, int S>
 hipError_t launch_tile(const GroupedArgs& a, hipStream_t s) {
   const int64_t grid = grid_blocks(a, BT, kGated ? BC / 2 : BC);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  grouped_kernel<T, kGated, kOut, BT, BC, WT, WC, S><<<dim3(static_cast<unsigned>(grid)), dim3(64 * WT * WC), 0, s>>>(a);
+  tile_kernel<T, kGated, kOut, BT, BC, WT, WC, S><<<dim3(static_cast<unsigned>(grid)), dim3(64 * WT * WC), 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -590,7 +846,8 @@ hipError_t launch_typed(const GroupedArgs& a, hipStream_t s) {
   int v = force;
   if (v == 0) v = per_group >= 128 ? 1 : per_group > 32 ? 2 : 6;
   switch (v) {
-    case 1: return launch_tile<T, kGated, kOut, 256, 256, 4, 2, 2>(a, s);
+    case 1: return launch_wide<T, kGated, kOut>(a, s);
+    case 15: return launch_tile<T, kGated, kOut, 256, 256, 4, 2, 2>(a, s);
     case 2: return launch_tile<T, kGated, kOut, 64, 128, 2, 2, 3>(a, s);
     case 3: return launch_stream<T, kGated, kOut, 1, F1, 8, 3>(a, s);
     case 4: return launch_tile<T, kGated, kOut, 64, 128, 2, 2, 4>(a, s);
