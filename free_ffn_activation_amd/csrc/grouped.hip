@@ -160,6 +160,21 @@ __device__ __forceinline__ Item uniform(const Item& i) {
           __builtin_amdgcn_readfirstlane(i.rows), __builtin_amdgcn_readfirstlane(i.channel_tile)};
 }
 
+// The gate's activation.  Both are z times a logistic function, z / (1 + e^-y):
+// y = z, and for the tanh form of GELU y = 2 sqrt(2/pi) (z + 0.044715 z^3), as
+// (1 + tanh(y / 2)) / 2 is that function of y.  Results of 16 bits take the
+// hardware's exponential and reciprocal: with the rounded argument they are off
+// by at most |y| 2^-23 relative, below 2^-16 while e^-y counts at all.
+template <int kOut>
+__device__ __forceinline__ float gate(float z, int act) {
+  if constexpr (kOut == PROX_F32) {
+    return gate_act(z, act);
+  } else {
+    const float y = act == PROX_ACT_SILU ? z : 1.5957691216057308f * (z + 0.044715f * z * z * z);
+    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y * -1.4426950408889634f));
+  }
+}
+
 // kCount neighbouring results from channel j on into the row of out at q; `left`
 // of them exist; vec: rows of out are 16-byte aligned (j is a multiple of kCount).
 template <int kOut, int kCount>
@@ -234,7 +249,8 @@ struct TileCopies {
   const float* scale;
   int kbytes, chunk, wave;
 
-  __device__ __forceinline__ void init(const GroupedArgs& a, const Item& it, int c0, int wave_, int lane) {
+  // *outside (LDS, 0 before): set if a row index of the tile is outside a.
+  __device__ __forceinline__ void init(const GroupedArgs& a, const Item& it, int c0, int wave_, int lane, int* outside) {
     const int crow = lane >> 3;
     chunk = ((lane & 7) ^ crow) * 16;
     wave = wave_;
@@ -252,8 +268,11 @@ struct TileCopies {
       woff[i] = static_cast<uint32_t>(j) * static_cast<uint32_t>(a.w_stride) + chunk;
     }
 #pragma unroll
-    for (int i = 0; i < NX; ++i)
-      xsrc[i] = a.a + max(source_row(a, it, (i * kWaves + wave) * 8 + crow), 0) * a.a_stride + chunk;
+    for (int i = 0; i < NX; ++i) {
+      const int src = source_row(a, it, (i * kWaves + wave) * 8 + crow);
+      if (src < 0) *outside = 1;
+      xsrc[i] = a.a + max(src, 0) * a.a_stride + chunk;
+    }
     scale = nullptr;
     if constexpr (kFp8) {
       if (wave < kTokenWaves) {
@@ -299,10 +318,11 @@ struct Places {
 // through the wave's own part of LDS, TP token fragments at a time, so that a row
 // of out is written in whole lines and the activation is one short loop (held in
 // registers it is unrolled to 40 KB of code, which every CU first has to fetch).
-// first: the wave's first channel; token_row(t): the tile's row of fragment t.
+// first: the wave's first channel; token_row(t): the tile's row of fragment t;
+// zeros: there are row indices outside a in the tile, whose results are zero.
 template <bool kGated, int kOut, int FC, int FT, int TP, typename Rows>
 __device__ __forceinline__ void write_results(const GroupedArgs& a, const Item& it, const f32x4_t (&acc)[FC][FT],
-                                              float* part, int lane, int first, Rows token_row) {
+                                              float* part, int lane, int first, bool zeros, Rows token_row) {
   constexpr int kStride = FC * 16 + 4;                 // floats per token: rows four banks apart
   constexpr int kChannels = FC * (kGated ? 8 : 16);    // results per token
   constexpr int kLanes = kChannels / 8, kPer = 64 / kLanes;  // lanes of a token, tokens at a time
@@ -326,15 +346,10 @@ __device__ __forceinline__ void write_results(const GroupedArgs& a, const Item& 
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = p[e];
       if constexpr (kGated) {
-        if (a.act == PROX_ACT_SILU) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= silu_f32(p[16 + e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= gelu_tanh_f32(p[16 + e]);
-        }
+        for (int e = 0; e < 8; ++e) v[e] *= gate<kOut>(p[16 + e], a.act);
       }
-      if (a.row_index && source_row(a, it, r) < 0) {  // a row index outside a: zeros
+      if (zeros && source_row(a, it, r) < 0) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
       }
@@ -361,7 +376,8 @@ __global__ void __launch_bounds__(64 * WT * WC) tile_kernel(GroupedArgs a) {
   constexpr uint32_t kLds = S * kBuffer > kWaves * kPart ? S * kBuffer : kWaves * kPart;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   __shared__ Item s_item;
-  __shared__ int s_total[kWaves];
+  __shared__ int s_total[kWaves], s_outside;
+  if (threadIdx.x == 0) s_outside = 0;  // find_item's barrier stands before its use
   const int chan_per_tile = kGated ? BC / 2 : BC;
   const int channel_tiles = (a.n + chan_per_tile - 1) / chan_per_tile;
   if (!find_item(a, BT, channel_tiles, &s_item, s_total)) return;
@@ -372,7 +388,7 @@ __global__ void __launch_bounds__(64 * WT * WC) tile_kernel(GroupedArgs a) {
   const int c0 = it.channel_tile * chan_per_tile;
   const int first = c0 + wc * FC * (kGated ? 8 : 16);
   Copies copies;
-  copies.init(a, it, c0, wave, lane);
+  copies.init(a, it, c0, wave, lane, &s_outside);
   const Places at(lane);
   const uint32_t lds0 = lds_offset(lds);
   // the block of 128 channels that this wave's lie in, from the tile's first on
@@ -477,7 +493,7 @@ __global__ void __launch_bounds__(64 * WT * WC) tile_kernel(GroupedArgs a) {
   multiply(std::false_type{}, std::true_type{}, kb, now, 0, 0);
   wait_copies_and_meet<0>();  // every wave has read its last step
   write_results<kGated, kOut, FC, FT, TP>(a, it, acc, reinterpret_cast<float*>(lds + wave * kPart), lane, first,
-                                          [&](int t) { return (wt * FT + t) * 16; });
+                                          s_outside != 0, [&](int t) { return (wt * FT + t) * 16; });
 }
 
 // Many rows per group: one block computes 256 tokens x 256 weight rows (gated:
@@ -493,7 +509,7 @@ __global__ void __launch_bounds__(64 * WT * WC) tile_kernel(GroupedArgs a) {
 // The waves take the token fragments in turn, so that a tile of at most 128
 // tokens (FT = 2) costs every wave half the products.
 template <typename T, bool kGated, int kOut, int FT>
-__device__ __forceinline__ void wide_tile(const GroupedArgs& a, const Item& it, uint8_t* lds, int c0) {
+__device__ __forceinline__ void wide_tile(const GroupedArgs& a, const Item& it, uint8_t* lds, int* outside, int c0) {
   constexpr int BT = FT * 64, BC = 256, WT = 4, kWaves = 8, FC = 8;
   constexpr bool kFp8 = std::is_same<T, Fp8Tag>::value;
   typedef TileCopies<kGated, kFp8, BT, BC, kWaves> Copies;
@@ -505,7 +521,7 @@ __device__ __forceinline__ void wide_tile(const GroupedArgs& a, const Item& it, 
   const int wc = wave / WT, wt = wave % WT;  // this wave's share of the channels and of the tokens
   const int first = c0 + wc * FC * (kGated ? 8 : 16);
   Copies copies;
-  copies.init(a, it, c0, wave, lane);
+  copies.init(a, it, c0, wave, lane, outside);
   const Places at(lane);
   const uint32_t lds0 = lds_offset(lds);
   const int block = first / kScaleBlock - c0 / kScaleBlock;  // this wave's block of 128 channels in the tile
@@ -634,7 +650,7 @@ __device__ __forceinline__ void wide_tile(const GroupedArgs& a, const Item& it, 
   multiply(std::false_type{}, std::true_type{}, kb, now, 0);
   wait_copies_and_meet<0>();  // every wave has read its last step
   write_results<kGated, kOut, FC, FT, 2>(a, it, acc, reinterpret_cast<float*>(lds + wave * kWidePart), lane, first,
-                                         [&](int t) { return (t * WT + wt) * 16; });
+                                         *outside != 0, [&](int t) { return (t * WT + wt) * 16; });
 }
 
 template <typename T, bool kGated, int kOut>
@@ -642,13 +658,14 @@ __global__ void __launch_bounds__(512) wide_kernel(GroupedArgs a) {
   constexpr uint32_t kBuffers = 2 * TileCopies<kGated, std::is_same<T, Fp8Tag>::value, 256, 256, 8>::kBuffer;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kBuffers > 8 * kWidePart ? kBuffers : 8 * kWidePart];
   __shared__ Item s_item;
-  __shared__ int s_total[8];
+  __shared__ int s_total[8], s_outside;
+  if (threadIdx.x == 0) s_outside = 0;  // find_item's barrier stands before its use
   const int chan_per_tile = kGated ? 128 : 256;
   const int channel_tiles = (a.n + chan_per_tile - 1) / chan_per_tile;
   if (!find_item(a, 256, channel_tiles, &s_item, s_total)) return;
   const Item it = uniform(s_item);
-  if (it.rows > 128) wide_tile<T, kGated, kOut, 4>(a, it, lds, it.channel_tile * chan_per_tile);
-  else wide_tile<T, kGated, kOut, 2>(a, it, lds, it.channel_tile * chan_per_tile);
+  if (it.rows > 128) wide_tile<T, kGated, kOut, 4>(a, it, lds, &s_outside, it.channel_tile * chan_per_tile);
+  else wide_tile<T, kGated, kOut, 2>(a, it, lds, &s_outside, it.channel_tile * chan_per_tile);
 }
 
 // Few rows per group: the weights stream from memory straight into the
@@ -682,9 +699,12 @@ __global__ void __launch_bounds__(64 * KW) stream_kernel(GroupedArgs a) {
   }
   const uint8_t* xsrc[FT];
   const float* xs[FT];
+  uint32_t outside = 0;  // bit t: this lane's row index of fragment t is outside a
 #pragma unroll
   for (int t = 0; t < FT; ++t) {
-    const int src = max(source_row(a, it, t * 16 + row), 0);
+    int src = source_row(a, it, t * 16 + row);
+    if (src < 0) outside |= 1u << t;
+    src = max(src, 0);
     xsrc[t] = a.a + src * a.a_stride + quad * 16;
     xs[t] = kFp8 ? a.a_scale + static_cast<int64_t>(src) * a.kblocks : nullptr;
   }
@@ -799,10 +819,10 @@ __global__ void __launch_bounds__(64 * KW) stream_kernel(GroupedArgs a) {
       z = part[0][(f + 1) * FT + t][lane];
       for (int w = 1; w < KW; ++w) z += part[w][(f + 1) * FT + t][lane];
     }
-    const bool none = source_row(a, it, r) < 0;
+    const bool none = outside >> t & 1;
     float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = none ? 0.f : kGated ? u[e] * gate_act(z[e], a.act) : u[e];
+    for (int e = 0; e < 4; ++e) v[e] = none ? 0.f : kGated ? u[e] * gate<kOut>(z[e], a.act) : u[e];
     const int j = c0 + (kGated ? f / 2 : f) * 16 + quad * 4;
     store_results<kOut, 4>(a.out + (static_cast<int64_t>(it.row0) + r) * a.out_stride, j, v, a.n - j, a.vec_out);
   }
