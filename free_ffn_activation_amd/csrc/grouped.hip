@@ -13,8 +13,6 @@
 // place c ^ (r % 8), so that the eight rows of a fragment read touch all banks.
 // The order of k inside a step does not matter as long as both sides agree, so
 // all three types read the same two 16-byte chunks per lane and step.
-#include <stdlib.h>
-
 #include "experts_internal.h"
 #include "prox_device.h"
 
@@ -858,47 +856,59 @@ hipError_t launch_tile(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Which kernel.  What the host knows: rows, groups and sizes, not how the rows
+// spread over the groups; m is the mean over the groups that can have any.  A tile
+// is taken if the mean fills it (else its products go to waste) and the launch
+// then has blocks for most of the CUs (else the next smaller tile, which spreads
+// the same work wider; with too few blocks even so, the streaming kernels, whose
+// waves share out k).  Measured (us; bf16, 64 groups, n 2048, k 1024 unless said):
+//   m 256: 256-token tiles 114, 128: 118, 64: 140      m 128: 86, 93, 88
+//   m 64:  64-token tiles 68, 128: > 75                 m 16: 53, 64 x 64 tiles 56
+//   one group, n = k = 4096: m 512: 64 x 128 tiles (256 blocks) 27.7, 128 x 128
+//     (128 blocks) 32.9; m 256: 64 x 64 (256) 22.0, 64 x 128 25.6; m 128: 32 x 64
+//     (256) 19.4, 64 x 64 20.7; m 16: streaming 13.4, 32 x 64 tiles (64) 18.9
+// fp32 products are bound by the matrix cores even in small tiles (256 flops per
+// clock and CU), so they go for many blocks first.
 template <typename T, bool kGated, int kOut>
-hipError_t launch_typed(const GroupedArgs& a, hipStream_t s) {
-  const int per_group = (a.rows + a.n_groups - 1) / a.n_groups;
+hipError_t launch_typed(const GroupedArgs& a, int cus, hipStream_t s) {
+  const int64_t live = std::min(a.n_groups, a.rows);
+  const int64_t m = (a.rows + live - 1) / live;
+  const int64_t n = static_cast<int64_t>(a.n) * (kGated ? 2 : 1);
+  const int steps = (a.kbytes + 127) / 128;
+  const auto blocks = [&](int bt, int bc) { return live * ((m + bt - 1) / bt) * ((n + bc - 1) / bc); };
   constexpr int F1 = kGated ? 2 : 1;
-  const int force = getenv("PX_FORCE") ? atoi(getenv("PX_FORCE")) : 0;
-  int v = force;
-  if (v == 0) v = per_group >= 128 ? 1 : per_group > 32 ? 2 : 6;
-  switch (v) {
-    case 1: return launch_wide<T, kGated, kOut>(a, s);
-    case 15: return launch_tile<T, kGated, kOut, 256, 256, 4, 2, 2>(a, s);
-    case 2: return launch_tile<T, kGated, kOut, 64, 128, 2, 2, 3>(a, s);
-    case 3: return launch_stream<T, kGated, kOut, 1, F1, 8, 3>(a, s);
-    case 4: return launch_tile<T, kGated, kOut, 64, 128, 2, 2, 4>(a, s);
-    case 5: return launch_stream<T, kGated, kOut, 1, 2, 4, 3>(a, s);
-    case 6: return launch_stream<T, kGated, kOut, 2, 2, 4, 2>(a, s);
-    case 7: return launch_stream<T, kGated, kOut, 2, 4, 4, 1>(a, s);
-    case 8: return launch_tile<T, kGated, kOut, 64, 64, 2, 2, 3>(a, s);
-    case 9: return launch_tile<T, kGated, kOut, 64, 64, 2, 2, 4>(a, s);
-    case 10: return launch_tile<T, kGated, kOut, 128, 128, 2, 2, 2>(a, s);
-    case 11: return launch_tile<T, kGated, kOut, 128, 128, 2, 2, 3>(a, s);
-    case 12: return launch_tile<T, kGated, kOut, 32, 64, 1, 2, 4>(a, s);
-    case 13: return launch_tile<T, kGated, kOut, 128, 256, 2, 4, 3>(a, s);
-    case 14: return launch_tile<T, kGated, kOut, 32, 64, 1, 2, 8>(a, s);
+  if constexpr (std::is_same<T, F32Tag>::value) {
+    if (m > 12 && blocks(64, 128) >= 2 * cus) return launch_tile<T, kGated, kOut, 64, 128, 2, 4, 3>(a, s);
+    if (m > 256 || (m > 12 && blocks(64, 64) >= cus * 3 / 4)) return launch_tile<T, kGated, kOut, 64, 64, 2, 2, 4>(a, s);
+    if (steps < 16 && blocks(32, 64) >= 2 * cus) return launch_tile<T, kGated, kOut, 32, 64, 1, 2, 4>(a, s);
+    if (m > 64) return launch_stream<T, kGated, kOut, 2, 2, 4, 2>(a, s);
+    if (kGated || blocks(16, 16) > cus) return launch_stream<T, kGated, kOut, 1, 2, 8, 2>(a, s);
+    return launch_stream<T, kGated, kOut, 1, F1, 16, 2>(a, s);
+  } else {
+    if (m >= 192 && blocks(256, 256) >= cus * 3 / 4) return launch_wide<T, kGated, kOut>(a, s);
+    if (m >= 96 && blocks(128, 256) >= cus * 5 / 8) return launch_tile<T, kGated, kOut, 128, 256, 2, 4, 3>(a, s);
+    if (m > 24 && blocks(64, 128) >= cus) return launch_tile<T, kGated, kOut, 64, 128, 2, 4, 3>(a, s);
+    if (m > 8 && blocks(64, 64) >= cus * 3 / 4) return launch_tile<T, kGated, kOut, 64, 64, 2, 2, 4>(a, s);
+    if (m > 64 || steps < 16 || blocks(32, 64) >= cus / 2)
+      return launch_tile<T, kGated, kOut, 32, 64, 1, 2, 4>(a, s);
+    if (!kGated && m <= 16 && steps >= 32) return launch_stream<T, kGated, kOut, 1, F1, 16, 2>(a, s);
+    return launch_stream<T, kGated, kOut, 1, 2, 8, 2>(a, s);
   }
-  return hipErrorInvalidValue;
 }
 
 template <typename T>
-hipError_t launch_type(const GroupedArgs& a, hipStream_t s) {
+hipError_t launch_type(const GroupedArgs& a, int cus, hipStream_t s) {
   if (a.out_dtype == PROX_F32)
-    return a.w_gate ? launch_typed<T, true, PROX_F32>(a, s) : launch_typed<T, false, PROX_F32>(a, s);
-  return a.w_gate ? launch_typed<T, true, PROX_BF16>(a, s) : launch_typed<T, false, PROX_BF16>(a, s);
+    return a.w_gate ? launch_typed<T, true, PROX_F32>(a, cus, s) : launch_typed<T, false, PROX_F32>(a, cus, s);
+  return a.w_gate ? launch_typed<T, true, PROX_BF16>(a, cus, s) : launch_typed<T, false, PROX_BF16>(a, cus, s);
 }
 
 }  // namespace
 
 hipError_t launch_grouped(const GroupedArgs& a, int cus, hipStream_t s) {
-  (void)cus;
-  if (a.wdtype == PROX_BF16) return launch_type<Bf16Tag>(a, s);
-  if (a.wdtype == PROX_F32) return launch_type<F32Tag>(a, s);
-  return launch_type<Fp8Tag>(a, s);
+  if (a.wdtype == PROX_BF16) return launch_type<Bf16Tag>(a, cus, s);
+  if (a.wdtype == PROX_F32) return launch_type<F32Tag>(a, cus, s);
+  return launch_type<Fp8Tag>(a, cus, s);
 }
 
 }  // namespace prox
