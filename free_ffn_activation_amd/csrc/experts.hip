@@ -26,22 +26,40 @@ __device__ __forceinline__ float route_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
-constexpr int kRouteThreads = 256;
+// Largest key of the wave, to every lane (DPP row shifts, then row broadcasts; a
+// lane whose source is outside its row reads 0, the smallest key).
+__device__ __forceinline__ uint32_t wave_max_key(uint32_t v) {
+#define PROX_MAX_STEP(ctrl, rows)                                                                     \
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), ctrl, rows, 0xF, false)))
+  PROX_MAX_STEP(0x111, 0xF);  // row_shr:1
+  PROX_MAX_STEP(0x112, 0xF);  // row_shr:2
+  PROX_MAX_STEP(0x114, 0xF);  // row_shr:4
+  PROX_MAX_STEP(0x118, 0xF);  // row_shr:8
+  PROX_MAX_STEP(0x142, 0xA);  // row_bcast:15
+  PROX_MAX_STEP(0x143, 0xC);  // row_bcast:31
+#undef PROX_MAX_STEP
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
+constexpr int kRouteThreads = 512;
 constexpr int kRouteSub = 64;      // tokens of one bitmap pass: the bits of a word
+constexpr int kRouteSmall = 32;    // tokens of a single-block launch, and of a block of a small launch
 constexpr int kRouteBlocks = 256;  // blocks at most
 
-// Tokens per block: whole passes of kRouteSub beyond kRouteBlocks blocks of 32.
+// Tokens per block: whole passes of kRouteSub beyond kRouteBlocks blocks of
+// kRouteSmall.
 __host__ __device__ inline int route_tokens_per_block(int tokens) {
-  if (tokens <= 32 * kRouteBlocks) return 32;
+  if (tokens <= kRouteSmall * kRouteBlocks) return kRouteSmall;
   const int per = (tokens + kRouteBlocks - 1) / kRouteBlocks;
   return (per + kRouteSub - 1) / kRouteSub * kRouteSub;
 }
 
 // The top_k of one token by one wave: kPer logits a lane, expert lane + 64 i.
-// Each round takes the largest key, the lowest expert among equals.
+// Each round takes the largest key by DPP (no LDS) and, by ballots, the lowest
+// expert that has it.  Returns this lane's slot's expert, or -1.
 template <int kPer>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int token, int lane) {
-  uint32_t key[kPer];
+__device__ __forceinline__ int route_token(const RouteArgs& a, int token, int lane) {
+  uint32_t key[kPer], all[kPer];
   const size_t base = static_cast<size_t>(token) * a.experts;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -50,35 +68,26 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int token, int l
     if (e < a.experts)
       key[i] = route_key(a.logits_dtype == PROX_F32 ? load_elem<F32Tag>(a.logits, base + e)
                                                     : load_elem<Bf16Tag>(a.logits, base + e));
+    all[i] = key[i];
   }
-  uint32_t all[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) all[i] = key[i];
   uint32_t my_key = 0;  // lane s holds slot s
   int my_id = -1;
   float top = 0.f;
   for (int s = 0; s < a.top_k; ++s) {
-    uint32_t best = 0;
-    int at = 0;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
-    // (key, lowest expert) as one 64-bit maximum
-    uint64_t v = (static_cast<uint64_t>(best) << 32) | static_cast<uint32_t>(~(lane + 64 * at));
+    for (int i = 1; i < kPer; ++i) best = max(best, key[i]);
+    best = wave_max_key(best);
+    if (best == 0) break;  // uniform: no expert is left
+    int e = 0;
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const uint64_t o = __shfl_xor(v, m);
-      v = o > v ? o : v;
+    for (int i = kPer - 1; i >= 0; --i) {
+      const uint64_t has = __ballot(key[i] == best);
+      if (has) e = 64 * i + __builtin_ctzll(has);
     }
-    const uint32_t k = static_cast<uint32_t>(v >> 32);
-    if (k == 0) break;  // uniform: no expert is left
-    const int e = static_cast<int>(~static_cast<uint32_t>(v));
-    if (s == 0) top = route_value(k);
+    if (s == 0) top = route_value(best);
     if (lane == s) {
-      my_key = k;
+      my_key = best;
       my_id = e;
     }
 #pragma unroll
@@ -99,35 +108,87 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int token, int l
     a.expert_idx[o] = my_id;
     a.weight[o] = my_id >= 0 ? p / total : 0.f;
   }
+  return my_id;
 }
 
-// The chosen experts of up to kRouteSub tokens from t0 on as one bitmap word
-// per expert (bit = token): a token takes an expert at most once, so the place
-// of (token, expert) among the tokens is a population count.
-__device__ __forceinline__ void route_bitmap(const RouteArgs& a, int t0, int nt, unsigned long long* bits) {
-  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) bits[e] = 0;
+// Exclusive sums of count[0 .. experts) into start, by the whole block; returns
+// the total.  Ends behind a barrier.
+__device__ __forceinline__ int route_offsets(const int* count, int* start, int experts, int* wave_total) {
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  const int per = (experts + nthr - 1) / nthr;  // neighbouring experts of a thread
+  int mine = 0;
+  for (int i = 0; i < per; ++i)
+    if (tid * per + i < experts) mine += count[tid * per + i];
+  int at = wave_inclusive_scan_int(mine);
+  if ((tid & 63) == 63) wave_total[tid >> 6] = at;
   __syncthreads();
-  for (int i = threadIdx.x; i < nt * a.top_k; i += kRouteThreads) {
-    const int t = i / a.top_k;
-    const int e = a.expert_idx[static_cast<size_t>(t0) * a.top_k + i];
-    if (e >= 0) atomicOr(&bits[e], 1ull << t);
+  at -= mine;
+  int rows = 0;
+  for (int w = 0; w < nthr >> 6; ++w) {
+    if (w < (tid >> 6)) at += wave_total[w];
+    rows += wave_total[w];
+  }
+  for (int i = 0; i < per; ++i)
+    if (tid * per + i < experts) {
+      start[tid * per + i] = at;
+      at += count[tid * per + i];
+    }
+  __syncthreads();
+  return rows;
+}
+
+// Up to kRouteSmall tokens: all in one block.  The chosen experts are kept as one
+// bitmap word per expert (bit = token): a token takes an expert at most once, so
+// its place among the expert's tokens is a population count.
+template <int kPer>
+__global__ void __launch_bounds__(1024) route_small_kernel(RouteArgs a) {
+  __shared__ uint32_t bits[kMaxExperts];
+  __shared__ int count[kMaxExperts], start[kMaxExperts];
+  __shared__ int wave_total[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e < a.experts; e += 1024) bits[e] = 0;
+  __syncthreads();
+  constexpr int kMine = kRouteSmall / 16;  // tokens of a wave
+  int id[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int t = wave + 16 * i;
+    id[i] = -1;
+    if (t < a.tokens) id[i] = route_token<kPer>(a, t, lane);
+    if (id[i] >= 0) atomicOr(&bits[id[i]], 1u << t);
   }
   __syncthreads();
+  for (int e = tid; e < a.experts; e += 1024) count[e] = __popc(bits[e]);
+  __syncthreads();
+  const int rows = route_offsets(count, start, a.experts, wave_total);
+  for (int e = tid; e < a.experts; e += 1024) a.offsets[e] = start[e];
+  if (tid == 0) a.offsets[a.experts] = rows;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int t = wave + 16 * i;
+    if (t >= a.tokens || lane >= a.top_k) continue;
+    int row = -1;
+    if (id[i] >= 0) {
+      row = start[id[i]] + __popc(bits[id[i]] & ((1u << t) - 1));
+      a.row_token[row] = t;
+    }
+    a.row_of[t * a.top_k + lane] = row;
+  }
+  for (int r = rows + tid; r < a.tokens * a.top_k; r += 1024) a.row_token[r] = -1;
 }
 
-// First launch: experts and weights of the block's tokens, and how many rows
-// each expert gets from them.
+// More tokens, first launch: experts and weights of the block's tokens, and how
+// many rows each expert gets from them.
 template <int kPer>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(RouteArgs a) {
   __shared__ int count[kMaxExperts];
   const int per = route_tokens_per_block(a.tokens);
   const int t0 = blockIdx.x * per, t1 = min(a.tokens, t0 + per);
   for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
-  const int lane = threadIdx.x & 63;
-  for (int t = t0 + (threadIdx.x >> 6); t < t1; t += kRouteThreads / 64) route_token<kPer>(a, t, lane);
   __syncthreads();
-  for (int i = threadIdx.x; i < (t1 - t0) * a.top_k; i += kRouteThreads) {
-    const int e = a.expert_idx[static_cast<size_t>(t0) * a.top_k + i];
+  const int lane = threadIdx.x & 63;
+  for (int t = t0 + (threadIdx.x >> 6); t < t1; t += kRouteThreads / 64) {
+    const int e = route_token<kPer>(a, t, lane);
     if (e >= 0) atomicAdd(&count[e], 1);
   }
   __syncthreads();
@@ -136,54 +197,54 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(RouteArgs a
 }
 
 // Second launch: every block adds up the counts of all blocks (so that no block
-// waits for another), then places its own rows.
+// waits for another), then places its own rows.  The counts are read by all
+// threads, kRouteThreads / experts blocks' rows side by side.
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(RouteArgs a, int blocks) {
-  __shared__ int next[kMaxExperts];   // the next row of each expert
+  __shared__ int next[kMaxExperts];   // rows of earlier blocks, then the next row of each expert
   __shared__ int total[kMaxExperts];
   __shared__ unsigned long long bits[kMaxExperts];
   __shared__ int wave_total[kRouteThreads / 64];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, me = blockIdx.x;
+  for (int e = tid; e < a.experts; e += kRouteThreads) next[e] = total[e] = 0;
+  __syncthreads();
+  {
+    const int side = max(1, kRouteThreads / a.experts);  // blocks' rows read side by side
+    const int lane_block = tid / a.experts;
+    for (int e0 = 0; e0 < a.experts; e0 += kRouteThreads) {  // one pass up to kRouteThreads experts
+      const int e = e0 + (side > 1 || a.experts == kRouteThreads ? tid % a.experts : tid);
+      if (e >= a.experts || (side > 1 && lane_block >= side)) continue;
+      const int* p = a.block_count + e;
+      int before = 0, sum = 0;
+#pragma unroll 8
+      for (int b = side > 1 ? lane_block : 0; b < blocks; b += side) {
+        const int c = p[static_cast<size_t>(b) * a.experts];
+        before += b < me ? c : 0;
+        sum += c;
+      }
+      atomicAdd(&next[e], before);
+      atomicAdd(&total[e], sum);
+    }
+  }
+  __syncthreads();
+  int* start = reinterpret_cast<int*>(bits);
+  const int rows = route_offsets(total, start, a.experts, wave_total);
   for (int e = tid; e < a.experts; e += kRouteThreads) {
-    int before = 0, sum = 0;
-    for (int b = 0; b < blocks; ++b) {
-      const int c = a.block_count[static_cast<size_t>(b) * a.experts + e];
-      if (b < static_cast<int>(blockIdx.x)) before += c;
-      sum += c;
-    }
-    next[e] = before;
-    total[e] = sum;
+    if (me == 0) a.offsets[e] = start[e];
+    next[e] += start[e];
   }
-  __syncthreads();
-  // exclusive sums over the experts: each thread a run of neighbouring ones
-  const int per = (a.experts + kRouteThreads - 1) / kRouteThreads;
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int e = tid * per + i;
-    if (e < a.experts) mine += total[e];
-  }
-  int start = wave_inclusive_scan_int(mine);
-  if ((tid & 63) == 63) wave_total[tid >> 6] = start;
-  __syncthreads();
-  start -= mine;
-  int rows = 0;
-  for (int w = 0; w < kRouteThreads / 64; ++w) {
-    if (w < (tid >> 6)) start += wave_total[w];
-    rows += wave_total[w];
-  }
-  for (int i = 0; i < per; ++i) {
-    const int e = tid * per + i;
-    if (e < a.experts) {
-      if (blockIdx.x == 0) a.offsets[e] = start;
-      next[e] += start;
-      start += total[e];
-    }
-  }
-  if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = rows;
+  if (me == 0 && tid == 0) a.offsets[a.experts] = rows;
   const int tpb = route_tokens_per_block(a.tokens);
-  const int t0 = blockIdx.x * tpb, t1 = min(a.tokens, t0 + tpb);
+  const int t0 = me * tpb, t1 = min(a.tokens, t0 + tpb);
   for (int s0 = t0; s0 < t1; s0 += kRouteSub) {
     const int nt = min(kRouteSub, t1 - s0);
-    route_bitmap(a, s0, nt, bits);  // its first barrier also covers next[]
+    __syncthreads();
+    for (int e = tid; e < a.experts; e += kRouteThreads) bits[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < nt * a.top_k; i += kRouteThreads) {
+      const int e = a.expert_idx[static_cast<size_t>(s0) * a.top_k + i];
+      if (e >= 0) atomicOr(&bits[e], 1ull << (i / a.top_k));
+    }
+    __syncthreads();
     for (int i = tid; i < nt * a.top_k; i += kRouteThreads) {
       const int t = i / a.top_k;
       const size_t o = static_cast<size_t>(s0) * a.top_k + i;
@@ -197,11 +258,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(RouteArgs a,
     }
     __syncthreads();
     for (int e = tid; e < a.experts; e += kRouteThreads) next[e] += __popcll(bits[e]);
-    __syncthreads();
   }
   // rows behind the last expert's
   const int all = a.tokens * a.top_k;
-  for (int r = rows + blockIdx.x * kRouteThreads + tid; r < all; r += blocks * kRouteThreads) a.row_token[r] = -1;
+  for (int r = rows + me * kRouteThreads + tid; r < all; r += blocks * kRouteThreads) a.row_token[r] = -1;
 }
 
 // ---------------------------------------------------------------- quantizer
@@ -382,14 +442,17 @@ size_t route_workspace(int tokens, int experts, int top_k) {
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   const int blocks = route_blocks(a.tokens);
-  const dim3 grid(blocks), block(kRouteThreads);
-  if (a.experts <= 64) route_choose_kernel<1><<<grid, block, 0, s>>>(a);
-  else if (a.experts <= 128) route_choose_kernel<2><<<grid, block, 0, s>>>(a);
-  else if (a.experts <= 256) route_choose_kernel<4><<<grid, block, 0, s>>>(a);
-  else route_choose_kernel<16><<<grid, block, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
+  const auto per = [&](auto kernel1, auto kernel2, auto kernel4, auto kernel16, int threads) {
+    const auto kernel = a.experts <= 64 ? kernel1 : a.experts <= 128 ? kernel2 : a.experts <= 256 ? kernel4 : kernel16;
+    kernel<<<dim3(blocks), dim3(threads), 0, s>>>(a);
+    return hipGetLastError();
+  };
+  if (blocks == 1)
+    return per(route_small_kernel<1>, route_small_kernel<2>, route_small_kernel<4>, route_small_kernel<16>, 1024);
+  const hipError_t e = per(route_choose_kernel<1>, route_choose_kernel<2>, route_choose_kernel<4>,
+                           route_choose_kernel<16>, kRouteThreads);
   if (e != hipSuccess) return e;
-  route_place_kernel<<<grid, block, 0, s>>>(a, blocks);
+  route_place_kernel<<<dim3(blocks), dim3(kRouteThreads), 0, s>>>(a, blocks);
   return hipGetLastError();
 }
 

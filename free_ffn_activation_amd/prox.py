@@ -504,24 +504,27 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
 
 
 def _flat(t, shape, dtype, name: str) -> int:
-    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, "
                          f"not {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _launch(fn, device: torch.device, tensors, stream, *args) -> None:
+def _launch(fn, lead: torch.Tensor, others, stream, *args) -> None:
     """fn(*args, stream) with the tensors' device as the current one."""
-    if device.type != "cuda":
+    device = lead.get_device()
+    if device < 0:
         raise ValueError("tensors must be on a GPU")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {t.device} and {device} in one call")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on {t.device} and {lead.device} in one call")
+    # the raw handle: a Stream object per call would cost as much as the launch
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if device == torch.cuda.current_device():
+        _check(fn(*args, handle))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)))
+            _check(fn(*args, handle))
 
 
 class ProxExperts:
@@ -581,7 +584,7 @@ def prox_grouped_matmul(experts: ProxExperts, a: torch.Tensor, out: torch.Tensor
         ps = _flat(a_scale, (a.shape[0], -(-experts.k // 128)), torch.float32, "a_scale")
     elif a_scale is not None:
         raise ValueError("a_scale is for float8 rows only")
-    _launch(_lib.prox_grouped_matmul, experts.device, (a, out, offsets, row_index, a_scale), stream,
+    _launch(_lib.prox_grouped_matmul, experts.tensors[0], (a, out, offsets, row_index, a_scale), stream,
             experts._ref, a.data_ptr(), a.shape[0], a_stride, ps, pi, po, rows, out.data_ptr(),
             _dtype_code(out, _OUT_TYPES, "out"), out_stride)
 
@@ -602,7 +605,7 @@ def prox_expert_route(logits: torch.Tensor, expert_idx: torch.Tensor, weight: to
     t, e = logits.shape
     k = expert_idx.shape[1]
     i32 = torch.int32
-    _launch(_lib.prox_expert_route, logits.device, (expert_idx, weight, offsets, row_token, row_of, ws), stream,
+    _launch(_lib.prox_expert_route, logits, (expert_idx, weight, offsets, row_token, row_of, ws), stream,
             logits.data_ptr(), _dtype_code(logits, _OUT_TYPES, "logits"), t, e, k, int(bool(renormalize)),
             _flat(expert_idx, (t, k), i32, "expert_idx"), _flat(weight, (t, k), torch.float32, "weight"),
             _flat(offsets, (e + 1,), i32, "offsets"), _flat(row_token, (t * k,), i32, "row_token"),
@@ -617,7 +620,7 @@ def prox_fp8_quantize(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, blo
         raise ValueError("q must be float8_e4m3fn of the shape of x")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
-    _launch(_lib.prox_fp8_quantize, x.device, (q, scale), stream, x.data_ptr(), _dtype_code(x, _OUT_TYPES, "x"), rows,
+    _launch(_lib.prox_fp8_quantize, x, (q, scale), stream, x.data_ptr(), _dtype_code(x, _OUT_TYPES, "x"), rows,
             k, xs, block_rows, q.data_ptr(), qs,
             _flat(scale, (-(-rows // block_rows), -(-k // 128)), torch.float32, "scale"))
 
@@ -629,7 +632,7 @@ def prox_expert_combine(h: torch.Tensor, row_of: torch.Tensor, weight: torch.Ten
     if row_of.dim() != 2 or y.shape != (row_of.shape[0], h.shape[1]):
         raise ValueError("row_of must be [tokens, top_k] and y [tokens, columns of h]")
     t, k = row_of.shape
-    _launch(_lib.prox_expert_combine, h.device, (row_of, weight, y), stream, h.data_ptr(),
+    _launch(_lib.prox_expert_combine, h, (row_of, weight, y), stream, h.data_ptr(),
             _dtype_code(h, _OUT_TYPES, "h"), h.shape[0], hs, _flat(row_of, (t, k), torch.int32, "row_of"),
             _flat(weight, (t, k), torch.float32, "weight"), t, k, h.shape[1], y.data_ptr(),
             _dtype_code(y, _OUT_TYPES, "y"), ys)
@@ -661,6 +664,6 @@ def prox_moe_ffn(layer: ProxMoeLayer, x: torch.Tensor, y: torch.Tensor, ws: torc
     if x.dim() != 2:
         raise ValueError("x must be [tokens, d_model]")
     shape = (x.shape[0], layer.up.k)
-    _launch(_lib.prox_moe_ffn, layer.device, (x, y, ws), stream, ctypes.byref(layer.desc),
+    _launch(_lib.prox_moe_ffn, layer.w_router, (x, y, ws), stream, ctypes.byref(layer.desc),
             _flat(x, shape, layer.x_dtype, "x"), shape[0], _flat(y, shape, torch.float32, "y"), _ptr(ws),
             ws.numel() * ws.element_size())
