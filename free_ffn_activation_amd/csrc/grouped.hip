@@ -13,6 +13,9 @@
 // place c ^ (r % 8), so that the eight rows of a fragment read touch all banks.
 // The order of k inside a step does not matter as long as both sides agree, so
 // all three types read the same two 16-byte chunks per lane and step.
+#include <algorithm>
+#include <cmath>
+
 #include "experts_internal.h"
 #include "prox_device.h"
 
@@ -318,12 +321,17 @@ struct Places {
 // registers it is unrolled to 40 KB of code, which every CU first has to fetch).
 // first: the wave's first channel; token_row(t): the tile's row of fragment t;
 // zeros: there are row indices outside a in the tile, whose results are zero.
-template <bool kGated, int kOut, int FC, int FT, int TP, typename Rows>
+// WK: that many waves, `group` the number of this one, hold parts of the same
+// results (each of a share of k), `apart` floats from part to part; they are added
+// up here, in the order of the groups, and the waves share the rows.
+template <bool kGated, int kOut, int FC, int FT, int TP, int WK, typename Rows>
 __device__ __forceinline__ void write_results(const GroupedArgs& a, const Item& it, const f32x4_t (&acc)[FC][FT],
-                                              float* part, int lane, int first, bool zeros, Rows token_row) {
+                                              float* part, int group, int apart, int lane, int first, bool zeros,
+                                              Rows token_row) {
   constexpr int kStride = FC * 16 + 4;                 // floats per token: rows four banks apart
   constexpr int kChannels = FC * (kGated ? 8 : 16);    // results per token
   constexpr int kLanes = kChannels / 8, kPer = 64 / kLanes;  // lanes of a token, tokens at a time
+  static_assert(WK == 1 || TP == FT, "the groups meet once");
   const int row = lane & 15, quad = lane >> 4;
   const int slot = lane / kLanes, j0 = lane % kLanes * 8;
   const int left = a.n - first - j0;  // results that exist from this lane's first on
@@ -333,9 +341,11 @@ __device__ __forceinline__ void write_results(const GroupedArgs& a, const Item& 
     for (int t = t0; t < t0 + TP; ++t)
 #pragma unroll
       for (int f = 0; f < FC; ++f)
-        *reinterpret_cast<f32x4_t*>(part + ((t - t0) * 16 + row) * kStride + f * 16 + quad * 4) = acc[f][t];
+        *reinterpret_cast<f32x4_t*>(part + group * apart + ((t - t0) * 16 + row) * kStride + f * 16 + quad * 4) =
+            acc[f][t];
+    if constexpr (WK > 1) __syncthreads();
 #pragma unroll 1
-    for (int i = slot; i < TP * 16; i += kPer) {
+    for (int i = slot + group * kPer; i < TP * 16; i += kPer * WK) {
       const int r = token_row(t0 + (i >> 4)) + (i & 15);
       if (r >= it.rows || left <= 0) continue;
       // a channel's up and gate are sixteen rows apart
@@ -343,9 +353,18 @@ __device__ __forceinline__ void write_results(const GroupedArgs& a, const Item& 
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = p[e];
-      if constexpr (kGated) {
+      for (int g = 1; g < WK; ++g)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= gate<kOut>(p[16 + e], a.act);
+        for (int e = 0; e < 8; ++e) v[e] += p[g * apart + e];
+      if constexpr (kGated) {
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = p[16 + e];
+        for (int g = 1; g < WK; ++g)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] += p[g * apart + 16 + e];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= gate<kOut>(z[e], a.act);
       }
       if (zeros && source_row(a, it, r) < 0) {
 #pragma unroll
@@ -358,10 +377,14 @@ __device__ __forceinline__ void write_results(const GroupedArgs& a, const Item& 
 }
 
 // One block: BT tokens x BC weight rows (gated: BC / 2 channels, up and gate in
-// turn by sixteen rows), WC x WT waves, S LDS buffers: while the waves multiply
-// step s, the copies of steps s + 1 .. s + S - 1 are under way.
-template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC, int S>
-__global__ void __launch_bounds__(64 * WT * WC) tile_kernel(GroupedArgs a) {
+// turn by sixteen rows), WK groups of WC x WT waves, S LDS buffers a group.  The
+// groups take the steps of k in turn: where a launch has too few blocks to fill
+// the chip, a block's time is its number of steps, each of which costs a latency.
+// While a group multiplies a step, the copies of its next S - 1 are under way.
+// (At least two waves per SIMD: with more registers the compiler moves the sums
+// between the two register files in every step.)
+template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC, int WK, int S>
+__global__ void __launch_bounds__(64 * WT * WC * WK, 2) tile_kernel(GroupedArgs a) {
   constexpr int kWaves = WT * WC, FC = BC / 16 / WC, FT = BT / 16 / WT;  // fragments of 16 per wave
   constexpr bool kFp8 = std::is_same<T, Fp8Tag>::value;
   typedef TileCopies<kGated, kFp8, BT, BC, kWaves> Copies;
@@ -369,26 +392,28 @@ __global__ void __launch_bounds__(64 * WT * WC) tile_kernel(GroupedArgs a) {
   static_assert(FC <= 8 && 128 % (FC * 16) == 0, "a wave's channels lie in one scale block");
   static_assert(!kGated || FC % 2 == 0, "up and gate of a channel belong to one wave");
   constexpr uint32_t kBuffer = Copies::kBuffer, kCopies = Copies::kCount;
-  constexpr int TP = FT < 2 ? FT : 2;                       // token fragments written at a time
+  constexpr int TP = FT < 2 || WK > 1 ? FT : 2;            // token fragments written at a time
   constexpr uint32_t kPart = TP * 16 * (FC * 16 + 4) * 4;  // LDS of a wave's results
-  constexpr uint32_t kLds = S * kBuffer > kWaves * kPart ? S * kBuffer : kWaves * kPart;
+  constexpr uint32_t kLds = WK * (S * kBuffer > kWaves * kPart ? S * kBuffer : kWaves * kPart);
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   __shared__ Item s_item;
-  __shared__ int s_total[kWaves], s_outside;
+  __shared__ int s_total[kWaves * WK], s_outside;
   if (threadIdx.x == 0) s_outside = 0;  // find_item's barrier stands before its use
   const int chan_per_tile = kGated ? BC / 2 : BC;
   const int channel_tiles = (a.n + chan_per_tile - 1) / chan_per_tile;
   if (!find_item(a, BT, channel_tiles, &s_item, s_total)) return;
   const Item it = uniform(s_item);
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int number = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = number / kWaves, wave = number % kWaves;
   const int wc = wave / WT, wt = wave % WT;  // this wave's share of the channels and of the tokens
   const int c0 = it.channel_tile * chan_per_tile;
   const int first = c0 + wc * FC * (kGated ? 8 : 16);
   Copies copies;
   copies.init(a, it, c0, wave, lane, &s_outside);
   const Places at(lane);
-  const uint32_t lds0 = lds_offset(lds);
+  uint8_t* const mine = lds + group * (S * kBuffer);  // the group's buffers
+  const uint32_t lds0 = lds_offset(mine);
   // the block of 128 channels that this wave's lie in, from the tile's first on
   const int block = first / kScaleBlock - c0 / kScaleBlock;
 
@@ -401,8 +426,8 @@ __global__ void __launch_bounds__(64 * WT * WC) tile_kernel(GroupedArgs a) {
   // Multiplies the step in buffer `from`, and meanwhile (more) issues the copies
   // of the step at next_kb into `to`, a few between the products.
   const auto multiply = [&](auto more, auto last, int kb, uint32_t from, int next_kb, uint32_t to) {
-    const uint8_t* pw = lds + from + (wc * FC * 16 + at.row) * 128;
-    const uint8_t* px = lds + from + BC * 128 + (wt * FT * 16 + at.row) * 128;
+    const uint8_t* pw = mine + from + (wc * FC * 16 + at.row) * 128;
+    const uint8_t* px = mine + from + BC * 128 + (wt * FT * 16 + at.row) * 128;
     const auto read = [&](const uint8_t* p) {
       Frag r = at.read(p);
       if constexpr (decltype(last)::value) {  // chunks past the end of k count as zeros
@@ -418,11 +443,16 @@ __global__ void __launch_bounds__(64 * WT * WC) tile_kernel(GroupedArgs a) {
     float xscale[FT], ws_up = 0.f, ws_gate = 0.f;
     f32x4_t part[2][FT];  // fp8: a fragment's products, scaled and added one fragment later
     if constexpr (kFp8) {
-      const float* ps = reinterpret_cast<const float*>(lds + from + Copies::kScales);
+      const float* ps = reinterpret_cast<const float*>(mine + from + Copies::kScales);
 #pragma unroll
       for (int t = 0; t < FT; ++t) xscale[t] = ps[(wt * FT + t) * 16 + at.row];
       ws_up = ps[Copies::kTokenWaves * 64 + block];
       ws_gate = kGated ? ps[Copies::kTokenWaves * 64 + Copies::kBlocks + block] : ws_up;
+      if (WK > 1 && decltype(last)::value && kb >= a.kbytes) {  // no step, no scales
+#pragma unroll
+        for (int t = 0; t < FT; ++t) xscale[t] = 0.f;
+        ws_up = ws_gate = 0.f;
+      }
     }
     const auto add = [&](int f) {
 #pragma unroll
@@ -461,37 +491,45 @@ __global__ void __launch_bounds__(64 * WT * WC) tile_kernel(GroupedArgs a) {
     }
     if constexpr (kFp8) add(FC - 1);
   };
+  const int steps = (a.kbytes + 127) / 128;
+  const auto copy = [&](int step, uint32_t to) {
+    const int kb = step * 128, off = copies.offset(kb);
+#pragma unroll
+    for (int c = 0; c < static_cast<int>(kCopies); ++c) copies.go(c, kb, off, lds0 + to);
+  };
   uint32_t now = 0, next = 0;  // the buffers of this step and of the next copy
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) {
-    if (i * 128 < a.kbytes) {
-      const int off = copies.offset(i * 128);
-#pragma unroll
-      for (int c = 0; c < static_cast<int>(kCopies); ++c) copies.go(c, i * 128, off, lds0 + next);
-    }
+    if (i * WK + group < steps) copy(i * WK + group, next);
     next += kBuffer;
   }
   const auto advance = [&] {
     next = next == (S - 1) * kBuffer ? 0 : next + kBuffer;
     now = now == (S - 1) * kBuffer ? 0 : now + kBuffer;
   };
-  int kb = 0;
-  for (; kb + (S - 1) * 128 < a.kbytes; kb += 128) {
+  // rounds of one step a group; as long as every group has a step to copy
+  int round = 0;
+  for (; (round + S) * WK <= steps; ++round) {
+    const int step = round * WK + group, then = step + (S - 1) * WK;
     // this step's copies are done when only those of the later steps are left
     wait_copies_and_meet<(S - 2) * kCopies>();
-    multiply(std::true_type{}, std::false_type{}, kb, now, kb + (S - 1) * 128, next);
+    multiply(std::true_type{}, std::false_type{}, step * 128, now, then * 128, next);
     advance();
   }
-  for (; kb + 128 < a.kbytes; kb += 128) {
+  for (; (round + 1) * WK < steps; ++round) {
+    const int step = round * WK + group, then = step + (S - 1) * WK;
     wait_copies_and_meet<0>();
-    multiply(std::false_type{}, std::false_type{}, kb, now, 0, 0);
+    if (then < steps) copy(then, next);
+    multiply(std::false_type{}, std::false_type{}, step * 128, now, 0, 0);
     advance();
   }
+  // the last round: a group without a step multiplies zeros
   wait_copies_and_meet<0>();
-  multiply(std::false_type{}, std::true_type{}, kb, now, 0, 0);
+  multiply(std::false_type{}, std::true_type{}, (round * WK + group) * 128, now, 0, 0);
   wait_copies_and_meet<0>();  // every wave has read its last step
-  write_results<kGated, kOut, FC, FT, TP>(a, it, acc, reinterpret_cast<float*>(lds + wave * kPart), lane, first,
-                                          s_outside != 0, [&](int t) { return (wt * FT + t) * 16; });
+  write_results<kGated, kOut, FC, FT, TP, WK>(a, it, acc, reinterpret_cast<float*>(lds + wave * kPart), group,
+                                              kWaves * kPart / 4, lane, first, s_outside != 0,
+                                              [&](int t) { return (wt * FT + t) * 16; });
 }
 
 // Many rows per group: one block computes 256 tokens x 256 weight rows (gated:
@@ -647,8 +685,8 @@ __device__ __forceinline__ void wide_tile(const GroupedArgs& a, const Item& it, 
   }
   multiply(std::false_type{}, std::true_type{}, kb, now, 0);
   wait_copies_and_meet<0>();  // every wave has read its last step
-  write_results<kGated, kOut, FC, FT, 2>(a, it, acc, reinterpret_cast<float*>(lds + wave * kWidePart), lane, first,
-                                         *outside != 0, [&](int t) { return (t * WT + wt) * 16; });
+  write_results<kGated, kOut, FC, FT, 2, 1>(a, it, acc, reinterpret_cast<float*>(lds + wave * kWidePart), 0, 0, lane,
+                                            first, *outside != 0, [&](int t) { return (t * WT + wt) * 16; });
 }
 
 template <typename T, bool kGated, int kOut>
@@ -666,178 +704,10 @@ __global__ void __launch_bounds__(512) wide_kernel(GroupedArgs a) {
   else wide_tile<T, kGated, kOut, 2>(a, it, lds, &s_outside, it.channel_tile * chan_per_tile);
 }
 
-// Few rows per group: the weights stream from memory straight into the
-// registers of the matrix cores, without LDS.  One block: FT x 16 tokens and FC x
-// 16 weight rows (gated: up and gate in turn), whose K is dealt out to KW waves
-// step by step; the waves' sums meet in LDS at the end, added in wave order.
-// While a wave multiplies U steps, the loads of the next U are under way.
-template <typename T, bool kGated, int kOut, int FT, int FC, int KW, int U>
-__global__ void __launch_bounds__(64 * KW) stream_kernel(GroupedArgs a) {
-  constexpr bool kFp8 = std::is_same<T, Fp8Tag>::value;
-  static_assert(!kGated || FC % 2 == 0, "up and gate of a channel belong together");
-  static_assert(FC <= 8, "a block's channels lie in one scale block");
-  __shared__ f32x4_t part[KW][FC * FT][64];
-  __shared__ Item s_item;
-  __shared__ int s_total[KW];
-  constexpr int kChannels = FC * (kGated ? 8 : 16);
-  const int channel_tiles = (a.n + kChannels - 1) / kChannels;
-  if (!find_item(a, FT * 16, channel_tiles, &s_item, s_total)) return;
-  const Item it = uniform(s_item);
-  const int lane = threadIdx.x & 63, row = lane & 15, quad = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c0 = it.channel_tile * kChannels;
-  const int64_t first = it.group * a.w_group + c0 * a.w_stride;
-  const uint8_t* const w_up = a.w + first;
-  const uint8_t* const w_gate = kGated ? a.w_gate + first : w_up;
-  uint32_t woff[FC];
-#pragma unroll
-  for (int f = 0; f < FC; ++f) {
-    const int j = min((kGated ? f / 2 : f) * 16 + row, a.n - 1 - c0);
-    woff[f] = static_cast<uint32_t>(j) * static_cast<uint32_t>(a.w_stride) + quad * 16;
-  }
-  const uint8_t* xsrc[FT];
-  const float* xs[FT];
-  uint32_t outside = 0;  // bit t: this lane's row index of fragment t is outside a
-#pragma unroll
-  for (int t = 0; t < FT; ++t) {
-    int src = source_row(a, it, t * 16 + row);
-    if (src < 0) outside |= 1u << t;
-    src = max(src, 0);
-    xsrc[t] = a.a + src * a.a_stride + quad * 16;
-    xs[t] = kFp8 ? a.a_scale + static_cast<int64_t>(src) * a.kblocks : nullptr;
-  }
-  const float *wsc_up = nullptr, *wsc_gate = nullptr;
-  if constexpr (kFp8) {
-    const int64_t block = (static_cast<int64_t>(it.group) * a.nblocks + c0 / kScaleBlock) * a.kblocks;
-    wsc_up = a.w_scale + block;
-    wsc_gate = kGated ? a.w_gate_scale + block : wsc_up;
-  }
-  f32x4_t acc[FC][FT];
-#pragma unroll
-  for (int f = 0; f < FC; ++f)
-#pragma unroll
-    for (int t = 0; t < FT; ++t) acc[f][t] = f32x4_t{0, 0, 0, 0};
-
-  struct Step {
-    Frag w[FC], x[FT];
-    float xscale[FT];
-  };
-  const auto load = [&](int step, Step& s) {
-    const int kb = step * 128;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int f = 0; f < FC; ++f)
-        s.w[f].c[h] = *reinterpret_cast<const u32x4_t*>((kGated && (f & 1) ? w_gate : w_up) + kb + woff[f] + h * 64);
-#pragma unroll
-      for (int t = 0; t < FT; ++t) s.x[t].c[h] = *reinterpret_cast<const u32x4_t*>(xsrc[t] + kb + h * 64);
-    }
-    if constexpr (kFp8) {
-#pragma unroll
-      for (int t = 0; t < FT; ++t) s.xscale[t] = xs[t][step];
-    }
-  };
-  const auto multiply = [&](int step, const Step& s) {
-    float ws_up = 0.f, ws_gate = 0.f;
-    if constexpr (kFp8) {
-      ws_up = wsc_up[step];
-      ws_gate = kGated ? wsc_gate[step] : ws_up;
-    }
-#pragma unroll
-    for (int f = 0; f < FC; ++f)
-#pragma unroll
-      for (int t = 0; t < FT; ++t) {
-        if constexpr (kFp8) {
-          const f32x4_t p = mma<T>(s.w[f], s.x[t], f32x4_t{0, 0, 0, 0});
-          const float sc = s.xscale[t] * (kGated && (f & 1) ? ws_gate : ws_up);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(p[i], sc, acc[f][t][i]);
-        } else {
-          acc[f][t] = mma<T>(s.w[f], s.x[t], acc[f][t]);
-        }
-      }
-  };
-  const int whole_steps = a.kbytes >> 7;
-  // this wave's steps: wave, wave + KW, ...; a step past the end repeats the
-  // wave's first one (or step 0) and is not multiplied
-  const int mine = whole_steps > wave ? (whole_steps - wave + KW - 1) / KW : 0;
-  Step buf[2][U];
-  const auto fetch = [&](int i0, Step* b) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) load(i0 + u < mine ? wave + (i0 + u) * KW : wave, b[u]);
-  };
-  if (mine > 0) {
-    fetch(0, buf[0]);
-    for (int i0 = 0; i0 < mine; i0 += 2 * U) {
-      if (i0 + U < mine) fetch(i0 + U, buf[1]);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + u < mine) multiply(wave + (i0 + u) * KW, buf[0][u]);
-      if (i0 + U >= mine) break;
-      if (i0 + 2 * U < mine) fetch(i0 + 2 * U, buf[0]);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + U + u < mine) multiply(wave + (i0 + U + u) * KW, buf[1][u]);
-    }
-  }
-  if ((a.kbytes & 127) && whole_steps % KW == wave) {  // the part of a step at the end of k
-    Step s;
-    const int kb = whole_steps * 128;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool in = kb + (h * 4 + quad) * 16 < a.kbytes;
-#pragma unroll
-      for (int f = 0; f < FC; ++f) {
-        const uint8_t* p = (kGated && (f & 1) ? w_gate : w_up) + kb + woff[f] + h * 64;
-        s.w[f].c[h] = *(in ? reinterpret_cast<const u32x4_t*>(p) : &g_zero16);
-      }
-#pragma unroll
-      for (int t = 0; t < FT; ++t)
-        s.x[t].c[h] = *(in ? reinterpret_cast<const u32x4_t*>(xsrc[t] + kb + h * 64) : &g_zero16);
-    }
-    if constexpr (kFp8) {
-#pragma unroll
-      for (int t = 0; t < FT; ++t) s.xscale[t] = xs[t][whole_steps];
-    }
-    multiply(whole_steps, s);
-  }
-#pragma unroll
-  for (int f = 0; f < FC; ++f)
-#pragma unroll
-    for (int t = 0; t < FT; ++t) part[wave][f * FT + t][lane] = acc[f][t];
-  __syncthreads();
-  constexpr int kSums = (kGated ? FC / 2 : FC) * FT;
-  for (int i = wave; i < kSums; i += KW) {
-    const int f = i / FT * (kGated ? 2 : 1), t = i % FT;
-    const int r = t * 16 + row;
-    if (r >= it.rows) continue;
-    f32x4_t u = part[0][f * FT + t][lane], z = f32x4_t{0, 0, 0, 0};
-    for (int w = 1; w < KW; ++w) u += part[w][f * FT + t][lane];
-    if constexpr (kGated) {
-      z = part[0][(f + 1) * FT + t][lane];
-      for (int w = 1; w < KW; ++w) z += part[w][(f + 1) * FT + t][lane];
-    }
-    const bool none = outside >> t & 1;
-    float v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = none ? 0.f : kGated ? u[e] * gate<kOut>(z[e], a.act) : u[e];
-    const int j = c0 + (kGated ? f / 2 : f) * 16 + quad * 4;
-    store_results<kOut, 4>(a.out + (static_cast<int64_t>(it.row0) + r) * a.out_stride, j, v, a.n - j, a.vec_out);
-  }
-}
-
 // Blocks of a launch: at least the items that offsets can make.
 int64_t grid_blocks(const GroupedArgs& a, int bt, int channels) {
   const int64_t tiles = a.rows / bt + std::min(a.n_groups, a.rows);
   return (tiles * ((a.n + channels - 1) / channels) + 7) / 8 * 8;
-}
-
-template <typename T, bool kGated, int kOut, int FT, int FC, int KW, int U>
-hipError_t launch_stream(const GroupedArgs& a, hipStream_t s) {
-  const int64_t grid = grid_blocks(a, FT * 16, FC * (kGated ? 8 : 16));
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  stream_kernel<T, kGated, kOut, FT, FC, KW, U><<<dim3(static_cast<unsigned>(grid)), dim3(64 * KW), 0, s>>>(a);
-  return hipGetLastError();
 }
 
 template <typename T, bool kGated, int kOut>
@@ -848,51 +718,78 @@ hipError_t launch_wide(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC, int S>
+template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC, int WK, int S>
 hipError_t launch_tile(const GroupedArgs& a, hipStream_t s) {
   const int64_t grid = grid_blocks(a, BT, kGated ? BC / 2 : BC);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  tile_kernel<T, kGated, kOut, BT, BC, WT, WC, S><<<dim3(static_cast<unsigned>(grid)), dim3(64 * WT * WC), 0, s>>>(a);
+  tile_kernel<T, kGated, kOut, BT, BC, WT, WC, WK, S>
+      <<<dim3(static_cast<unsigned>(grid)), dim3(64 * WT * WC * WK), 0, s>>>(a);
   return hipGetLastError();
 }
 
-// Which kernel.  What the host knows: rows, groups and sizes, not how the rows
-// spread over the groups; m is the mean over the groups that can have any.  A tile
-// is taken if the mean fills it (else its products go to waste) and the launch
-// then has blocks for most of the CUs (else the next smaller tile, which spreads
-// the same work wider; with too few blocks even so, the streaming kernels, whose
-// waves share out k).  Measured (us; bf16, 64 groups, n 2048, k 1024 unless said):
-//   m 256: 256-token tiles 114, 128: 118, 64: 140      m 128: 86, 93, 88
-//   m 64:  64-token tiles 68, 128: > 75                 m 16: 53, 64 x 64 tiles 56
-//   one group, n = k = 4096: m 512: 64 x 128 tiles (256 blocks) 27.7, 128 x 128
-//     (128 blocks) 32.9; m 256: 64 x 64 (256) 22.0, 64 x 128 25.6; m 128: 32 x 64
-//     (256) 19.4, 64 x 64 20.7; m 16: streaming 13.4, 32 x 64 tiles (64) 18.9
-// fp32 products are bound by the matrix cores even in small tiles (256 flops per
-// clock and CU), so they go for many blocks first.
+// Which kernel.  A block's time is its rounds of steps times the time of one: a
+// latency while the launch leaves CUs idle, and a share of the CU once there are
+// several blocks to each.  The shape with the smallest estimate,
+//   rounds * max(latency, blocks / CUs * cost),
+// is taken.  What the host knows is rows, groups and sizes, not how the rows
+// spread: a group of m rows on average counts as m / tokens + 1/2 tiles.  The
+// figures (us a step) are those that choose best on MI355X over 920 products of 1
+// to 64 groups, 1 to 1024 rows a group, n 256 to 12288 and k 256 to 12288: 3 % from
+// the best of all shapes in the mean for 16- and 8-bit types, 8 % for fp32 (by
+// thresholds on m and on the number of blocks: 6 and 12 %).  For example (bf16,
+// us): 64 groups, n 2048, k 1024, m 256: wide 114, 64 x 128 tiles 140; m 16: 64 x 128
+// 53, wide 60; one group, n = k = 4096, m 128: 32 x 64 in one K group 20, 32 x 32 in
+// four 15.
+enum Shape { kWide, k128x256, k64x128, k64x64, k32x64, k32x32by2, k32x32by4, kShapes };
+struct ShapeTime {
+  int tokens, channels, groups;  // a block's tile, and how many groups of waves share k
+  float latency, cost;
+};
+constexpr ShapeTime kTimes[kShapes] = {
+    {256, 256, 1, 2.0f, 2.4f},  {128, 256, 1, 1.2f, 1.6f},  {64, 128, 1, 0.45f, 0.51f}, {64, 64, 1, 0.30f, 0.29f},
+    {32, 64, 1, 0.26f, 0.23f},  {32, 32, 2, 0.25f, 0.25f},  {32, 32, 4, 0.43f, 0.71f}};
+// fp32 products are bound by the matrix cores (256 flops per clock and CU) even in
+// small tiles; the two large shapes are not built for them
+constexpr ShapeTime kTimesF32[kShapes] = {
+    {0, 0, 0, 0, 0},            {0, 0, 0, 0, 0},            {64, 128, 1, 1.12f, 1.35f}, {64, 64, 1, 0.61f, 0.72f},
+    {32, 64, 1, 0.61f, 0.50f},  {32, 32, 2, 0.47f, 0.43f},  {32, 32, 4, 0.68f, 0.89f}};
+
+Shape choose_shape(const GroupedArgs& a, int cus) {
+  const ShapeTime* times = a.wdtype == PROX_F32 ? kTimesF32 : kTimes;
+  const int live = std::min(a.n_groups, a.rows);  // groups that can have rows
+  const double n = static_cast<double>(a.n) * (a.w_gate ? 2 : 1);
+  const int steps = (a.kbytes + 127) / 128;
+  int best = k64x128;
+  double least = 0;
+  for (int i = 0; i < kShapes; ++i) {
+    const ShapeTime& t = times[i];
+    if (t.tokens == 0) continue;
+    const double tiles = live == 1 ? (a.rows + t.tokens - 1) / t.tokens
+                                   : live * std::max(1.0, static_cast<double>(a.rows) / live / t.tokens + 0.5);
+    const double blocks = tiles * std::ceil(n / t.channels);
+    const double time =
+        (steps + t.groups - 1) / t.groups * std::max<double>(t.latency, blocks / cus * t.cost);
+    if (least == 0 || time < least) {
+      least = time;
+      best = i;
+    }
+  }
+  return static_cast<Shape>(best);
+}
+
 template <typename T, bool kGated, int kOut>
 hipError_t launch_typed(const GroupedArgs& a, int cus, hipStream_t s) {
-  const int64_t live = std::min(a.n_groups, a.rows);
-  const int64_t m = (a.rows + live - 1) / live;
-  const int64_t n = static_cast<int64_t>(a.n) * (kGated ? 2 : 1);
-  const int steps = (a.kbytes + 127) / 128;
-  const auto blocks = [&](int bt, int bc) { return live * ((m + bt - 1) / bt) * ((n + bc - 1) / bc); };
-  constexpr int F1 = kGated ? 2 : 1;
-  if constexpr (std::is_same<T, F32Tag>::value) {
-    if (m > 12 && blocks(64, 128) >= 2 * cus) return launch_tile<T, kGated, kOut, 64, 128, 2, 4, 3>(a, s);
-    if (m > 256 || (m > 12 && blocks(64, 64) >= cus * 3 / 4)) return launch_tile<T, kGated, kOut, 64, 64, 2, 2, 4>(a, s);
-    if (steps < 16 && blocks(32, 64) >= 2 * cus) return launch_tile<T, kGated, kOut, 32, 64, 1, 2, 4>(a, s);
-    if (m > 64) return launch_stream<T, kGated, kOut, 2, 2, 4, 2>(a, s);
-    if (kGated || blocks(16, 16) > cus) return launch_stream<T, kGated, kOut, 1, 2, 8, 2>(a, s);
-    return launch_stream<T, kGated, kOut, 1, F1, 16, 2>(a, s);
-  } else {
-    if (m >= 192 && blocks(256, 256) >= cus * 3 / 4) return launch_wide<T, kGated, kOut>(a, s);
-    if (m >= 96 && blocks(128, 256) >= cus * 5 / 8) return launch_tile<T, kGated, kOut, 128, 256, 2, 4, 3>(a, s);
-    if (m > 24 && blocks(64, 128) >= cus) return launch_tile<T, kGated, kOut, 64, 128, 2, 4, 3>(a, s);
-    if (m > 8 && blocks(64, 64) >= cus * 3 / 4) return launch_tile<T, kGated, kOut, 64, 64, 2, 2, 4>(a, s);
-    if (m > 64 || steps < 16 || blocks(32, 64) >= cus / 2)
-      return launch_tile<T, kGated, kOut, 32, 64, 1, 2, 4>(a, s);
-    if (!kGated && m <= 16 && steps >= 32) return launch_stream<T, kGated, kOut, 1, F1, 16, 2>(a, s);
-    return launch_stream<T, kGated, kOut, 1, 2, 8, 2>(a, s);
+  const Shape shape = choose_shape(a, cus);
+  if constexpr (!std::is_same<T, F32Tag>::value) {
+    if (shape == kWide) return launch_wide<T, kGated, kOut>(a, s);
+    if (shape == k128x256) return launch_tile<T, kGated, kOut, 128, 256, 2, 4, 1, 3>(a, s);
+  }
+  switch (shape) {
+    case k64x64: return launch_tile<T, kGated, kOut, 64, 64, 2, 2, 1, 4>(a, s);
+    case k32x64: return launch_tile<T, kGated, kOut, 32, 64, 1, 2, 1, 4>(a, s);
+    case k32x32by2: return launch_tile<T, kGated, kOut, 32, 32, 2, 1, 2, 4>(a, s);
+    case k32x32by4: return launch_tile<T, kGated, kOut, 32, 32, 2, 1, 4, 3>(a, s);
+    default: return launch_tile<T, kGated, kOut, 64, 128, 2, 4, 1, 3>(a, s);
   }
 }
 
