@@ -490,6 +490,8 @@ def _dtype_code(t: torch.Tensor, types: dict, name: str) -> int:
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Elements between the rows of a 2-D tensor with contiguous rows."""
+    if t.is_contiguous() and t.dim() == 2:
+        return t.shape[1]
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
     s0, s1 = t.stride()
@@ -520,11 +522,13 @@ def _launch(fn, lead: torch.Tensor, others, stream, *args) -> None:
             raise ValueError(f"tensors on {t.device} and {lead.device} in one call")
     # the raw handle: a Stream object per call would cost as much as the launch
     handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    if device == torch.cuda.current_device():
-        _check(fn(*args, handle))
+    if device == torch._C._cuda_getDevice():
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, handle))
+            status = fn(*args, handle)
+    if status != PROX_OK:
+        _check(status)
 
 
 class ProxExperts:
