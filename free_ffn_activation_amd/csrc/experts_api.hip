@@ -76,7 +76,6 @@ GroupedArgs grouped_args(const prox_experts* e, const void* a, int a_rows, int64
   g.wdtype = e->wdtype;
   g.out_dtype = out_dtype;
   g.act = e->activation;
-  g.vec_out = aligned(out, 16) && g.out_stride % 16 == 0;
   return g;
 }
 

@@ -27,7 +27,6 @@ struct GroupedArgs {
   int a_rows, rows, n_groups, n, kbytes;
   int kblocks, nblocks;      // fp8 scale blocks of k and of n
   int wdtype, out_dtype, act;
-  int vec_out;               // rows of out are 16-byte aligned
 };
 hipError_t launch_grouped(const GroupedArgs& a, int cus, hipStream_t s);
 

@@ -177,27 +177,29 @@ __device__ __forceinline__ float gate(float z, int act) {
 }
 
 // kCount neighbouring results from channel j on into the row of out at q; `left`
-// of them exist; vec: rows of out are 16-byte aligned (j is a multiple of kCount).
+// of them exist.  Rows of out need their element's alignment only: the hardware
+// takes wide stores at any address.
 template <int kOut, int kCount>
-__device__ __forceinline__ void store_results(uint8_t* q, int j, const float (&v)[kCount], int left, bool vec) {
+__device__ __forceinline__ void store_results(uint8_t* q, int j, const float (&v)[kCount], int left) {
   if constexpr (kOut == PROX_F32) {
+    typedef __attribute__((ext_vector_type(4), aligned(4))) float vec_t;
     float* p = reinterpret_cast<float*>(q) + j;
-    if (vec && left >= kCount) {
+    if (left >= kCount) {
 #pragma unroll
       for (int h = 0; h < kCount; h += 4)
-        *reinterpret_cast<f32x4_t*>(p + h) = f32x4_t{v[h], v[h + 1], v[h + 2], v[h + 3]};
+        *reinterpret_cast<vec_t*>(p + h) = vec_t{v[h], v[h + 1], v[h + 2], v[h + 3]};
     } else {
 #pragma unroll
       for (int i = 0; i < kCount; ++i)
         if (i < left) p[i] = v[i];
     }
   } else {
-    typedef __attribute__((ext_vector_type(kCount))) __bf16 vec_t;
+    typedef __attribute__((ext_vector_type(kCount), aligned(2))) __bf16 vec_t;
     __bf16* p = reinterpret_cast<__bf16*>(q) + j;
     vec_t b;
 #pragma unroll
     for (int i = 0; i < kCount; ++i) b[i] = (__bf16)v[i];
-    if (vec && left >= kCount) {
+    if (left >= kCount) {
       *reinterpret_cast<vec_t*>(p) = b;
     } else {
 #pragma unroll
@@ -371,7 +373,7 @@ __device__ __forceinline__ void write_results(const GroupedArgs& a, const Item& 
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
       }
       uint8_t* q = a.out + (static_cast<int64_t>(it.row0) + r) * a.out_stride;
-      store_results<kOut, 8>(q, first + j0, v, left, a.vec_out);
+      store_results<kOut, 8>(q, first + j0, v, left);
     }
   }
 }
