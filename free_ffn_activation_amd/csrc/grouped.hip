@@ -96,64 +96,62 @@ struct Item {
   int group, row0, rows, channel_tile;  // rows: those of the tile, 1 .. BT
 };
 
-// The (token tile, channel tile) of this block.  Items run group by group;
-// within a group the token tiles run fastest.  Blocks go round the eight XCDs,
-// each with an L2 of its own: XCD x takes the x-th eighth of the items, so that
-// the blocks that share a group's weights share an L2.  False: no item is left.
-__device__ __forceinline__ bool find_item(const GroupedArgs& a, int bt, int channel_tiles, Item* shared,
-                                          int* wave_total) {
-  const int tid = threadIdx.x, nthr = blockDim.x;
-  const int xcd = blockIdx.x & 7, nth = blockIdx.x >> 3;
+// The rows [lo, hi) of a group, inside [0, rows) whatever the offsets say.
+__device__ __forceinline__ void group_rows(const GroupedArgs& a, int g, int* lo, int* hi) {
   if (a.offsets == nullptr) {
-    const int tiles = (a.rows + bt - 1) / bt, items = tiles * channel_tiles;
-    const int share = (items + 7) >> 3, item = xcd * share + nth;
-    if (nth >= share || item >= items) return false;
-    if (tid == 0) {
-      const int m = item % tiles;
-      *shared = {0, m * bt, min(bt, a.rows - m * bt), item / tiles};
-    }
-    __syncthreads();
-    return true;
+    *lo = 0;
+    *hi = a.rows;
+  } else {
+    *lo = min(max(a.offsets[g], 0), a.rows);
+    *hi = min(max(a.offsets[g + 1], *lo), a.rows);
   }
-  const int per = (a.n_groups + nthr - 1) / nthr;
-  const int g0 = tid * per;
+}
+
+// The (token tile of kTile, channel tile) of this block.  Items run group by group;
+// within a group the token tiles run fastest.  Blocks go round the eight XCDs, each
+// with an L2 of its own: XCD x takes the x-th eighth of the items, so that the
+// blocks that share a group's weights share an L2.  False: no item is left.  (If
+// offsets do not ascend, tiles may be left out, but none is outside the buffers.)
+template <int kTile>
+__device__ __forceinline__ bool find_item(const GroupedArgs& a, int channel_tiles, Item* shared, int* wave_total) {
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  const int per = (a.n_groups + nthr - 1) / nthr, g0 = tid * per;  // neighbouring groups of a thread
+  const int g1 = min(g0 + per, a.n_groups);
   int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int g = g0 + i;
-    if (g < a.n_groups) {
-      const int lo = min(max(a.offsets[g], 0), a.rows), hi = min(max(a.offsets[g + 1], lo), a.rows);
-      mine += (hi - lo + bt - 1) / bt;
-    }
+  for (int g = g0; g < g1; ++g) {
+    int lo, hi;
+    group_rows(a, g, &lo, &hi);
+    mine += (hi - lo + kTile - 1) / kTile;
   }
   int before = wave_inclusive_scan_int(mine);
   if ((tid & 63) == 63) wave_total[tid >> 6] = before;
+  if (tid == 0) shared->rows = 0;
   __syncthreads();
-  int total = 0;
   before -= mine;
+  int total = 0;
   for (int w = 0; w < nthr >> 6; ++w) {
     if (w < (tid >> 6)) before += wave_total[w];
     total += wave_total[w];
   }
-  const int items = total * channel_tiles;
-  const int share = (items + 7) >> 3, item = xcd * share + nth;
+  const int64_t items = static_cast<int64_t>(total) * channel_tiles, share = (items + 7) >> 3;
+  const int64_t nth = blockIdx.x >> 3, item = (blockIdx.x & 7) * share + nth;
   if (nth >= share || item >= items) return false;
-  if (item >= before * channel_tiles && item < (before + mine) * channel_tiles) {
-    for (int i = 0; i < per; ++i) {
-      const int g = g0 + i;
-      if (g >= a.n_groups) break;
-      const int lo = min(max(a.offsets[g], 0), a.rows), hi = min(max(a.offsets[g + 1], lo), a.rows);
-      const int tiles = (hi - lo + bt - 1) / bt;
-      const int rem = item - before * channel_tiles;
-      if (rem < tiles * channel_tiles) {
-        const int m = rem % tiles;
-        *shared = {g, lo + m * bt, min(bt, hi - lo - m * bt), rem / tiles};
+  int64_t rem = item - static_cast<int64_t>(before) * channel_tiles;
+  if (rem >= 0 && rem < static_cast<int64_t>(mine) * channel_tiles) {
+    for (int g = g0; g < g1; ++g) {
+      int lo, hi;
+      group_rows(a, g, &lo, &hi);
+      const int tiles = (hi - lo + kTile - 1) / kTile;
+      if (rem < static_cast<int64_t>(tiles) * channel_tiles) {
+        const int r = static_cast<int>(rem), m = r % tiles;  // below the launch's grid
+        *shared = {g, lo + m * kTile, min(kTile, hi - lo - m * kTile), r / tiles};
         break;
       }
-      before += tiles;
+      rem -= static_cast<int64_t>(tiles) * channel_tiles;
     }
   }
   __syncthreads();
-  return true;
+  return shared->rows > 0;
 }
 
 __device__ __forceinline__ Item uniform(const Item& i) {
@@ -403,7 +401,7 @@ __global__ void __launch_bounds__(64 * WT * WC * WK, 2) tile_kernel(GroupedArgs 
   if (threadIdx.x == 0) s_outside = 0;  // find_item's barrier stands before its use
   const int chan_per_tile = kGated ? BC / 2 : BC;
   const int channel_tiles = (a.n + chan_per_tile - 1) / chan_per_tile;
-  if (!find_item(a, BT, channel_tiles, &s_item, s_total)) return;
+  if (!find_item<BT>(a, channel_tiles, &s_item, s_total)) return;
   const Item it = uniform(s_item);
   const int lane = threadIdx.x & 63;
   const int number = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -700,7 +698,7 @@ __global__ void __launch_bounds__(512) wide_kernel(GroupedArgs a) {
   if (threadIdx.x == 0) s_outside = 0;  // find_item's barrier stands before its use
   const int chan_per_tile = kGated ? 128 : 256;
   const int channel_tiles = (a.n + chan_per_tile - 1) / chan_per_tile;
-  if (!find_item(a, 256, channel_tiles, &s_item, s_total)) return;
+  if (!find_item<256>(a, channel_tiles, &s_item, s_total)) return;
   const Item it = uniform(s_item);
   if (it.rows > 128) wide_tile<T, kGated, kOut, 4>(a, it, lds, &s_outside, it.channel_tile * chan_per_tile);
   else wide_tile<T, kGated, kOut, 2>(a, it, lds, &s_outside, it.channel_tile * chan_per_tile);

@@ -163,6 +163,76 @@ def test_product_inner_sizes(k, dtype):
         p.check(f"k {k} rows {rows}")
 
 
+# (rows of the groups, outputs): together with k and gating these take every tile
+# shape that the products choose among (from 32 x 32 in four groups of waves to
+# 256 x 256, whose last tiles have more or less than half their tokens)
+LARGE = [([700, 3, 0, 900], 1045), ([2100, 0, 129, 128, 1, 700], 2052), ([4000], 2306)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("i", range(len(LARGE)))
+@pytest.mark.parametrize("bytes_k", [16, 128, 144, 256, 272, 384, 1040, 2064])
+def test_product_large(dtype, gated, i, bytes_k):
+    """Many rows, against fp64 products on the GPU, for k of one step of 128 bytes,
+    of two, three and more, whole and in part."""
+    sizes, n = LARGE[i]
+    size = {"f32": 4, "bf16": 2, "fp8": 1}[dtype]
+    k = bytes_k // size
+    rows = sum(sizes) + 7
+    g = torch.Generator(device="cuda")
+    g.manual_seed(bytes_k + i)
+    kw = dict(device="cuda", generator=g)
+    src = torch.randint(0, 501, (rows,), dtype=torch.int32, **kw)
+    src[5], src[rows - 9] = -1, 501
+    a = torch.randn(501, k, **kw).to(DT[dtype])
+    ws = [(torch.randn(len(sizes), n, k, **kw) * 2 / k ** 0.5).to(DT[dtype]) for _ in range(1 + gated)]
+    blocks = (len(sizes), -(-n // 128), -(-k // 128))
+    scales = [torch.rand(blocks, **kw) + 0.5 for _ in ws] if dtype == "fp8" else [None] * len(ws)
+    a_scale = torch.rand(501, blocks[2], **kw) + 0.5 if dtype == "fp8" else None
+    off = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device="cuda")
+    out = torch.full((rows, n), 7.0, device="cuda", dtype=torch.float32)
+    e = P.ProxExperts(ws[0], ws[1] if gated else None, scale=scales[0], gate_scale=scales[-1] if gated else None)
+    P.prox_grouped_matmul(e, a, out, offsets=off, row_index=src, a_scale=a_scale)
+    assert (out[rows - 7:] == 7.0).all()
+    wide = [w.double() if s is None else
+            w.double() * s.double().repeat_interleave(128, 1)[:, :n].repeat_interleave(128, 2)[:, :, :k] for w, s in zip(ws, scales)]
+    x = a.double() if a_scale is None else a.double() * a_scale.double().repeat_interleave(128, 1)[:, :k]
+    x = torch.where(((src >= 0) & (src < 501))[:, None], x[src.clamp(0, 500).long()], 0.0)
+
+    def eights(t):  # the largest of eight neighbours: their product bounds that of _largest_of_8
+        return torch.nn.functional.pad(t.abs(), (0, -k % 8)).unflatten(-1, (-1, 8)).amax(-1)
+    c = (k + 8) * 2 * EPS
+    lo = 0
+    for j, m in enumerate(sizes):
+        hi = lo + m
+        val = [x[lo:hi] @ w[j].T for w in wide]
+        err = [c * (x[lo:hi].abs() @ w[j].abs().T) for w in wide]
+        if dtype == "fp8":
+            err = [r + 2.0 ** -10 * (eights(x[lo:hi]) @ eights(w[j]).T) for r, w in zip(err, wide)]
+        if gated:
+            u, z = val
+            ref = u * z * torch.sigmoid(z)
+            bound = err[0] * (z.abs() + err[1]) + 1.2 * err[1] * (u.abs() + err[0]) + 32 * EPS * u.abs() * z.abs()
+        else:
+            ref, bound = val[0], err[0]
+        bad = ~((out[lo:hi].double() - ref).abs() <= bound + 1e-37)
+        assert not bad.any(), f"group {j}: {int(bad.sum())} off, first at {torch.nonzero(bad)[0].tolist()}"
+        lo = hi
+
+
+def test_product_offsets_that_do_not_ascend():
+    """Contract broken, bounds kept: nothing outside out is written and the call ends."""
+    p = Product("bf16", [20, 20, 20], 64, 64, seed=2)
+    big = torch.full((100, 64), 3.0, device="cuda", dtype=torch.bfloat16)
+    off = torch.tensor([60, 0, 60, 0], device="cuda", dtype=torch.int32)
+    P.prox_grouped_matmul(p.experts, p.ta, big[20:80], offsets=off)
+    off = torch.tensor([0, 60, 0, 60], device="cuda", dtype=torch.int32)
+    P.prox_grouped_matmul(p.experts, p.ta, big[20:80], offsets=off)
+    torch.cuda.synchronize()
+    assert (big[:20] == 3).all() and (big[80:] == 3).all()
+
+
 def test_product_reads_a_decode_layers_pair():
     """Up and gate rows in turn, the w_upgate_t order of a decode layer."""
     for act in (P.PROX_ACT_SILU, P.PROX_ACT_GELU_TANH):
