@@ -166,7 +166,7 @@ def test_product_inner_sizes(k, dtype):
 # (rows of the groups, outputs): together with k and gating these take every tile
 # shape that the products choose among (from 32 x 32 in four groups of waves to
 # 256 x 256, whose last tiles have more or less than half their tokens)
-LARGE = [([700, 3, 0, 900], 1045), ([2100, 0, 129, 128, 1, 700], 2052), ([4000], 2306)]
+LARGE = [([700, 3, 0, 900], 1045), ([2100, 0, 129, 128, 1, 700], 2052), ([4000], 2306), ([600, 0, 140], 4101)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
