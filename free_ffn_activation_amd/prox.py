@@ -476,50 +476,45 @@ def prox_set_wait_limit(ticks: int) -> int:
 
 # ------------------------------------------------------------- routed FFN
 # These calls check shapes, types and devices here and launch on the tensors'
-# device.  Rows may be strided (the last dimension must be contiguous).
+# device.  Rows may be strided (the last dimension must be contiguous).  The
+# checks read each tensor property once: for the smallest calls they and the
+# launch are the whole time.
 _EXPERT_TYPES = {torch.float32: PROX_F32, torch.bfloat16: PROX_BF16, torch.float8_e4m3fn: PROX_FP8}
 _OUT_TYPES = {torch.float32: PROX_F32, torch.bfloat16: PROX_BF16}
+_I32, _FLOAT = torch.int32, torch.float32
 
 
-def _dtype_code(t: torch.Tensor, types: dict, name: str) -> int:
-    code = types.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} is {t.dtype}, expected one of {', '.join(str(v) for v in types)}")
-    return code
+def _no_type(t: torch.Tensor, types: dict, name: str) -> TypeError:
+    return TypeError(f"{name} is {t.dtype}, expected one of {', '.join(str(v) for v in types)}")
 
 
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between the rows of a 2-D tensor with contiguous rows."""
-    if t.is_contiguous() and t.dim() == 2:
-        return t.shape[1]
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
+def _matrix(t: torch.Tensor, name: str) -> tuple:
+    """(rows, columns, elements between rows) of a 2-D tensor with contiguous rows."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, not {len(shape)}")
+    rows, cols = shape
+    if t.is_contiguous() or rows <= 1 and (cols <= 1 or t.stride(1) == 1):
+        return rows, cols, cols  # the stride of a single row is not used
     s0, s1 = t.stride()
-    rows, cols = t.shape
     if cols > 1 and s1 != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    if rows <= 1:
-        return cols  # the stride of a single row is not used
     if s0 < cols:
         raise ValueError(f"the rows of {name} overlap")
-    return s0
+    return rows, cols, s0
 
 
-def _flat(t, shape, dtype, name: str) -> int:
+def _flat(t: torch.Tensor, shape: tuple, dtype, name: str) -> int:
+    """The address of a contiguous tensor of that shape and type."""
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, "
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"not {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _launch(fn, lead: torch.Tensor, others, stream, *args) -> None:
-    """fn(*args, stream) with the tensors' device as the current one."""
-    device = lead.get_device()
-    if device < 0:
-        raise ValueError("tensors must be on a GPU")
-    for t in others:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"tensors on {t.device} and {lead.device} in one call")
+def _launch(fn, device: int, stream, *args) -> None:
+    """fn(*args, stream) with the tensors' device (of every one of them) as the
+    current one."""
     # the raw handle: a Stream object per call would cost as much as the launch
     handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
     if device == torch._C._cuda_getDevice():
@@ -529,6 +524,17 @@ def _launch(fn, lead: torch.Tensor, others, stream, *args) -> None:
             status = fn(*args, handle)
     if status != PROX_OK:
         _check(status)
+
+
+def _device_of(lead: torch.Tensor, *others) -> int:
+    """The device of the tensors; refuses host tensors and mixed devices."""
+    device = lead.get_device()
+    if device < 0:
+        raise ValueError("tensors must be on a GPU")
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on {t.device} and {lead.device} in one call")
+    return device
 
 
 class ProxExperts:
@@ -544,7 +550,9 @@ class ProxExperts:
         if w.dim() != 3:
             raise ValueError("w must be [n_groups, n, k]")
         self.n_groups, self.n, self.k = (int(v) for v in w.shape)
-        self.wdtype = _dtype_code(w, _EXPERT_TYPES, "w")
+        if w.dtype not in _EXPERT_TYPES:
+            raise _no_type(w, _EXPERT_TYPES, "w")
+        self.wdtype, self.dtype = _EXPERT_TYPES[w.dtype], w.dtype
         if self.k > 1 and w.stride(2) != 1:
             raise ValueError("the rows of w must be contiguous")
         if w_gate is not None and (w_gate.shape != w.shape or w_gate.dtype != w.dtype or w_gate.device != w.device or
@@ -556,7 +564,7 @@ class ProxExperts:
             raise ValueError("float8 weights need a scale for each matrix, other weights take none")
         for t, name in ((scale, "scale"), (gate_scale, "gate_scale")):
             if t is not None:
-                _flat(t, blocks, torch.float32, name)
+                _flat(t, blocks, _FLOAT, name)
                 if t.device != w.device:
                     raise ValueError(f"{name} is on {t.device}, w on {w.device}")
         self.device, self.activation = w.device, activation
@@ -573,24 +581,28 @@ def prox_grouped_matmul(experts: ProxExperts, a: torch.Tensor, out: torch.Tensor
                         stream=None) -> None:
     """out[r] = a[row_index[r]] @ experts.w[g].T for the rows r of group g
     (offsets[g] <= r < offsets[g + 1]); gated experts: up times act(gate)."""
-    rows = out.shape[0]
-    a_stride, out_stride = _row_stride(a, "a"), _row_stride(out, "out")
-    if a.shape[1] != experts.k or _dtype_code(a, _EXPERT_TYPES, "a") != experts.wdtype:
-        raise ValueError(f"a must be [rows, {experts.k}] in the type of the weights, not {a.dtype} {tuple(a.shape)}")
-    if out.shape[1] != experts.n:
+    rows, n, out_stride = _matrix(out, "out")
+    a_rows, k, a_stride = _matrix(a, "a")
+    if k != experts.k or a.dtype != experts.dtype:
+        raise ValueError(f"a must be [rows, {experts.k}] in {experts.dtype}, not {a.dtype} {tuple(a.shape)}")
+    if n != experts.n:
         raise ValueError(f"out must be [rows, {experts.n}], not {tuple(out.shape)}")
-    po = _flat(offsets, (experts.n_groups + 1,), torch.int32, "offsets") if offsets is not None else None
-    pi = _flat(row_index, (rows,), torch.int32, "row_index") if row_index is not None else None
-    ps = None
+    out_type = _OUT_TYPES.get(out.dtype)
+    if out_type is None:
+        raise _no_type(out, _OUT_TYPES, "out")
+    po = pi = ps = None
+    if offsets is not None:
+        po = _flat(offsets, (experts.n_groups + 1,), _I32, "offsets")
+    if row_index is not None:
+        pi = _flat(row_index, (rows,), _I32, "row_index")
     if experts.wdtype == PROX_FP8:
         if a_scale is None:
             raise ValueError("float8 rows need a_scale")
-        ps = _flat(a_scale, (a.shape[0], -(-experts.k // 128)), torch.float32, "a_scale")
+        ps = _flat(a_scale, (a_rows, -(-k // 128)), _FLOAT, "a_scale")
     elif a_scale is not None:
         raise ValueError("a_scale is for float8 rows only")
-    _launch(_lib.prox_grouped_matmul, experts.tensors[0], (a, out, offsets, row_index, a_scale), stream,
-            experts._ref, a.data_ptr(), a.shape[0], a_stride, ps, pi, po, rows, out.data_ptr(),
-            _dtype_code(out, _OUT_TYPES, "out"), out_stride)
+    _launch(_lib.prox_grouped_matmul, _device_of(experts.tensors[0], a, out, offsets, row_index, a_scale), stream,
+            experts._ref, a.data_ptr(), a_rows, a_stride, ps, pi, po, rows, out.data_ptr(), out_type, out_stride)
 
 
 def prox_expert_route_workspace_size(n_tokens: int, n_experts: int, top_k: int) -> int:
@@ -604,42 +616,51 @@ def prox_expert_route(logits: torch.Tensor, expert_idx: torch.Tensor, weight: to
                       stream=None) -> None:
     """The top_k experts of every token (top_k: the columns of expert_idx),
     their weights, and the rows by expert."""
-    if logits.dim() != 2 or expert_idx.dim() != 2 or not logits.is_contiguous():
+    shape = expert_idx.shape
+    if len(logits.shape) != 2 or len(shape) != 2 or not logits.is_contiguous() or shape[0] != logits.shape[0]:
         raise ValueError("logits must be contiguous [tokens, experts], expert_idx [tokens, top_k]")
     t, e = logits.shape
-    k = expert_idx.shape[1]
-    i32 = torch.int32
-    _launch(_lib.prox_expert_route, logits, (expert_idx, weight, offsets, row_token, row_of, ws), stream,
-            logits.data_ptr(), _dtype_code(logits, _OUT_TYPES, "logits"), t, e, k, int(bool(renormalize)),
-            _flat(expert_idx, (t, k), i32, "expert_idx"), _flat(weight, (t, k), torch.float32, "weight"),
-            _flat(offsets, (e + 1,), i32, "offsets"), _flat(row_token, (t * k,), i32, "row_token"),
-            _flat(row_of, (t, k), i32, "row_of"), _ptr(ws), ws.numel() * ws.element_size())
+    k = shape[1]
+    logits_type = _OUT_TYPES.get(logits.dtype)
+    if logits_type is None:
+        raise _no_type(logits, _OUT_TYPES, "logits")
+    _launch(_lib.prox_expert_route, _device_of(logits, expert_idx, weight, offsets, row_token, row_of, ws), stream,
+            logits.data_ptr(), logits_type, t, e, k, 1 if renormalize else 0,
+            _flat(expert_idx, shape, _I32, "expert_idx"), _flat(weight, shape, _FLOAT, "weight"),
+            _flat(offsets, (e + 1,), _I32, "offsets"), _flat(row_token, (t * k,), _I32, "row_token"),
+            _flat(row_of, shape, _I32, "row_of"), _ptr(ws), ws.numel() * ws.element_size())
 
 
 def prox_fp8_quantize(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1, stream=None) -> None:
     """q = e4m3(x / scale), scale = amax / 448 of each block_rows x 128 block."""
-    xs, qs = _row_stride(x, "x"), _row_stride(q, "q")
-    rows, k = x.shape
-    if q.shape != x.shape or q.dtype != torch.float8_e4m3fn:
+    rows, k, xs = _matrix(x, "x")
+    q_rows, q_k, qs = _matrix(q, "q")
+    if q_rows != rows or q_k != k or q.dtype != torch.float8_e4m3fn:
         raise ValueError("q must be float8_e4m3fn of the shape of x")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
-    _launch(_lib.prox_fp8_quantize, x, (q, scale), stream, x.data_ptr(), _dtype_code(x, _OUT_TYPES, "x"), rows,
-            k, xs, block_rows, q.data_ptr(), qs,
-            _flat(scale, (-(-rows // block_rows), -(-k // 128)), torch.float32, "scale"))
+    x_type = _OUT_TYPES.get(x.dtype)
+    if x_type is None:
+        raise _no_type(x, _OUT_TYPES, "x")
+    _launch(_lib.prox_fp8_quantize, _device_of(x, q, scale), stream, x.data_ptr(), x_type, rows, k, xs, block_rows,
+            q.data_ptr(), qs, _flat(scale, (-(-rows // block_rows), -(-k // 128)), _FLOAT, "scale"))
 
 
 def prox_expert_combine(h: torch.Tensor, row_of: torch.Tensor, weight: torch.Tensor, y: torch.Tensor,
                         stream=None) -> None:
     """y[t] = sum over slots s of weight[t, s] * h[row_of[t, s]]."""
-    hs, ys = _row_stride(h, "h"), _row_stride(y, "y")
-    if row_of.dim() != 2 or y.shape != (row_of.shape[0], h.shape[1]):
+    h_rows, n, hs = _matrix(h, "h")
+    t, y_n, ys = _matrix(y, "y")
+    shape = row_of.shape
+    if len(shape) != 2 or shape[0] != t or y_n != n:
         raise ValueError("row_of must be [tokens, top_k] and y [tokens, columns of h]")
-    t, k = row_of.shape
-    _launch(_lib.prox_expert_combine, h, (row_of, weight, y), stream, h.data_ptr(),
-            _dtype_code(h, _OUT_TYPES, "h"), h.shape[0], hs, _flat(row_of, (t, k), torch.int32, "row_of"),
-            _flat(weight, (t, k), torch.float32, "weight"), t, k, h.shape[1], y.data_ptr(),
-            _dtype_code(y, _OUT_TYPES, "y"), ys)
+    k = shape[1]
+    h_type, y_type = _OUT_TYPES.get(h.dtype), _OUT_TYPES.get(y.dtype)
+    if h_type is None or y_type is None:
+        raise _no_type(h if h_type is None else y, _OUT_TYPES, "h" if h_type is None else "y")
+    _launch(_lib.prox_expert_combine, _device_of(h, row_of, weight, y), stream, h.data_ptr(), h_type, h_rows, hs,
+            _flat(row_of, shape, _I32, "row_of"), _flat(weight, shape, _FLOAT, "weight"), t, k, n, y.data_ptr(), y_type,
+            ys)
 
 
 class ProxMoeLayer:
@@ -654,6 +675,7 @@ class ProxMoeLayer:
         self.w_router, self.up, self.down, self.top_k = w_router, up, down, top_k
         self.x_dtype, self.device = want, w_router.device
         self.desc = prox_moe_layer(up.desc, down.desc, w_router.data_ptr(), top_k, int(bool(renormalize)), 0)
+        self._ref = ctypes.byref(self.desc)
         prox_moe_workspace_size(self, 1)  # the library's own checks of the layer
 
 
@@ -668,6 +690,6 @@ def prox_moe_ffn(layer: ProxMoeLayer, x: torch.Tensor, y: torch.Tensor, ws: torc
     if x.dim() != 2:
         raise ValueError("x must be [tokens, d_model]")
     shape = (x.shape[0], layer.up.k)
-    _launch(_lib.prox_moe_ffn, layer.w_router, (x, y, ws), stream, ctypes.byref(layer.desc),
-            _flat(x, shape, layer.x_dtype, "x"), shape[0], _flat(y, shape, torch.float32, "y"), _ptr(ws),
+    _launch(_lib.prox_moe_ffn, _device_of(layer.w_router, x, y, ws), stream, layer._ref,
+            _flat(x, shape, layer.x_dtype, "x"), shape[0], _flat(y, shape, _FLOAT, "y"), _ptr(ws),
             ws.numel() * ws.element_size())
