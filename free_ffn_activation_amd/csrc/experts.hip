@@ -488,7 +488,7 @@ hipError_t launch_combine_typed(const CombineArgs& a, hipStream_t s) {
   const int threads = std::min(256, ((a.n + kVec - 1) / kVec + 63) / 64 * 64);
   const int per = (a.n + kVec * threads - 1) / (kVec * threads);
   const int64_t grid = static_cast<int64_t>(a.tokens) * per;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (!grid_fits(grid, threads)) return hipErrorInvalidConfiguration;
   combine_kernel<T, kOut, kVec><<<dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s>>>(a, per);
   return hipGetLastError();
 }
@@ -532,7 +532,7 @@ hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s) {
   const int64_t kblocks = (a.k + kScaleBlock - 1) / kScaleBlock;
   const int64_t grid = a.block_rows == 1 ? (a.rows * kblocks + 31) / 32
                                          : (a.rows + kScaleBlock - 1) / kScaleBlock * kblocks;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (!grid_fits(grid, 256)) return hipErrorInvalidConfiguration;
   const dim3 g(static_cast<unsigned>(grid)), b(256);
   if (a.block_rows == 1) {
     if (a.x_dtype == PROX_F32) quantize_rows_kernel<F32Tag><<<g, b, 0, s>>>(a, static_cast<int>(kblocks));

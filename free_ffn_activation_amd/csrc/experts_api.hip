@@ -10,10 +10,14 @@ namespace prox {
 namespace {
 
 constexpr int64_t kMaxRows = int64_t{1} << 30;
+constexpr int kMaxDim = 1 << 24;                  // n and k
+constexpr int64_t kMaxStride = int64_t{1} << 40;  // elements; keeps the sizes in bytes inside 64 bits
+constexpr int64_t kMaxWeightRow = 1 << 23;        // bytes: the products' offsets inside a tile have 32 bits
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 int elem(int dtype) { return dtype == PROX_F32 ? 4 : dtype == PROX_BF16 ? 2 : 1; }
+bool stride_fits(int64_t s) { return s >= -kMaxStride && s <= kMaxStride; }
 int blocks128(int v) { return (v + kScaleBlock - 1) / kScaleBlock; }
 
 prox_status check_experts(const prox_experts* e) {
@@ -26,13 +30,15 @@ prox_status check_experts(const prox_experts* e) {
                 e->activation);
   if (e->n_groups < 1 || e->n < 1 || e->k < 1)
     return fail(PROX_ERR_INVALID_ARG, "experts n_groups %d, n %d and k %d must be positive", e->n_groups, e->n, e->k);
-  if (e->n_groups > kMaxExperts || e->n > (1 << 24) || e->k > (1 << 24))
+  if (e->n_groups > kMaxExperts || e->n > kMaxDim || e->k > kMaxDim)
     return fail(PROX_ERR_UNSUPPORTED, "experts n_groups %d above %d, or n %d or k %d above 2^24", e->n_groups,
                 kMaxExperts, e->n, e->k);
+  if (!stride_fits(e->row_stride) || !stride_fits(e->group_stride))
+    return fail(PROX_ERR_UNSUPPORTED, "experts strides must be at most 2^40 elements");
   const int es = elem(e->wdtype);
   if (static_cast<int64_t>(e->k) * es % 16 != 0 || e->row_stride * es % 16 != 0 || e->group_stride * es % 16 != 0)
     return fail(PROX_ERR_UNSUPPORTED, "experts k and strides must be multiples of 16 bytes");
-  if (e->row_stride * es >= (1 << 23))
+  if (e->row_stride * es >= kMaxWeightRow)
     return fail(PROX_ERR_UNSUPPORTED, "experts row_stride must be below 8 MiB");
   if (e->row_stride < e->k || e->group_stride < 0)
     return fail(PROX_ERR_INVALID_ARG, "experts row_stride is below k or group_stride is negative");
@@ -141,6 +147,8 @@ prox_status check_moe(const prox_moe_layer* L, int32_t n_tokens) {
   const int es = L->up.wdtype == PROX_F32 ? 4 : 2;  // type of x, the router and the rows between the products
   if (L->up.k * es % 16 != 0 || L->up.n * es % 16 != 0)
     return fail(PROX_ERR_UNSUPPORTED, "layer d_model %d and d_ff %d must be multiples of 16 bytes", L->up.k, L->up.n);
+  if (static_cast<int64_t>(L->up.k) * es >= kMaxWeightRow)  // a row of w_router, which may be wider than up's
+    return fail(PROX_ERR_UNSUPPORTED, "layer d_model %d: rows of w_router must be below 8 MiB", L->up.k);
   if (!L->w_router || !aligned(L->w_router, 16))
     return fail(PROX_ERR_INVALID_ARG, "layer w_router must be non-NULL and 16-byte aligned");
   return check_route_shape(n_tokens, L->up.n_groups, L->top_k);
@@ -169,6 +177,8 @@ PROX_API prox_status prox_grouped_matmul(const prox_experts* e, const void* a, i
     const int es = elem(e->wdtype);
     if (a_stride < e->k || out_stride < e->n)
       return fail(PROX_ERR_INVALID_ARG, "a_stride below k or out_stride below n");
+    if (a_stride > kMaxStride || out_stride > kMaxStride)
+      return fail(PROX_ERR_UNSUPPORTED, "strides must be at most 2^40 elements");
     if (a_stride * es % 16 != 0) return fail(PROX_ERR_UNSUPPORTED, "a_stride must be a multiple of 16 bytes");
     if (rows == 0) return PROX_OK;
     if (a_rows == 0) return fail(PROX_ERR_INVALID_ARG, "a_rows is 0 with %d rows", rows);
@@ -247,11 +257,13 @@ PROX_API prox_status prox_fp8_quantize(const void* x, int32_t x_dtype, int32_t r
     clear_error();
     if (x_dtype != PROX_F32 && x_dtype != PROX_BF16)
       return fail(PROX_ERR_INVALID_ARG, "x_dtype %d is neither PROX_F32 nor PROX_BF16", x_dtype);
-    if (rows < 0 || rows > kMaxRows || k < 1 || k > (1 << 24))
+    if (rows < 0 || rows > kMaxRows || k < 1 || k > kMaxDim)
       return fail(PROX_ERR_INVALID_ARG, "rows %d outside [0, 2^30] or k %d outside [1, 2^24]", rows, k);
     if (block_rows != 1 && block_rows != kScaleBlock)
       return fail(PROX_ERR_INVALID_ARG, "block_rows %d is neither 1 nor 128", block_rows);
     if (x_stride < k || q_stride < k) return fail(PROX_ERR_INVALID_ARG, "x_stride or q_stride below k");
+    if (x_stride > kMaxStride || q_stride > kMaxStride)
+      return fail(PROX_ERR_UNSUPPORTED, "strides must be at most 2^40 elements");
     if (k % 16 != 0 || q_stride % 16 != 0 || x_stride * elem(x_dtype) % 16 != 0)
       return fail(PROX_ERR_UNSUPPORTED, "k must be a multiple of 16 and the strides multiples of 16 bytes");
     if (rows == 0) return PROX_OK;
@@ -309,6 +321,8 @@ PROX_API prox_status prox_expert_combine(const void* h, int32_t h_dtype, int32_t
       return fail(PROX_ERR_INVALID_ARG, "n_tokens %d, h_rows %d, top_k %d (1..%d) or n %d out of range", n_tokens, h_rows,
                   top_k, kMaxTopK, n);
     if (h_stride < n || y_stride < n) return fail(PROX_ERR_INVALID_ARG, "h_stride or y_stride below n");
+    if (n > kMaxDim || h_stride > kMaxStride || y_stride > kMaxStride)
+      return fail(PROX_ERR_UNSUPPORTED, "n %d above 2^24, or strides above 2^40 elements", n);
     if (n_tokens == 0) return PROX_OK;
     if (!y || !row_of || !weight || (h_rows > 0 && !h))
       return fail(PROX_ERR_INVALID_ARG, "h, row_of, weight and y must be non-NULL");
@@ -407,7 +421,7 @@ PROX_API prox_status prox_moe_ffn(const prox_moe_layer* L, const void* x, int32_
       xs = reinterpret_cast<float*>(base + p.xs);
     }
     // the rows between the products are stored in x's type: half the traffic of
-    // fp32 at one rounding of 2^-9 relative, as a layer of that type stores them
+    // fp32 at one rounding of 2^-8 relative, as a layer of that type stores them
     void* h = base + p.h;
     e = launch_grouped(grouped_args(&L->up, a, n_tokens, d, xs, row_token, offsets, rows, h, xdtype, f), cus, s);
     if (e != hipSuccess) return hip_fail(e, "up/gate product launch");

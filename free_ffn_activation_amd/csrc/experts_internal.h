@@ -10,6 +10,11 @@ constexpr int kMaxExperts = 1024;  // experts of a router, groups of a product
 constexpr int kMaxTopK = 32;
 constexpr int kScaleBlock = 128;   // values that share one fp8 scale
 
+// Whether a grid can be launched: blocks, and threads in all, have 32 bits.
+inline bool grid_fits(int64_t blocks, int threads) {
+  return blocks <= 0x7FFFFFFF && blocks * threads <= 0xFFFFFFFFll;
+}
+
 // Products of ragged groups of rows, out[r] = a[src(r)] W_g^T for the rows r of
 // group g.  Strides are in bytes; every row of a and w starts 16-byte aligned
 // and holds kbytes (a multiple of 16) bytes.

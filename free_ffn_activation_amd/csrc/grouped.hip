@@ -713,7 +713,7 @@ int64_t grid_blocks(const GroupedArgs& a, int bt, int channels) {
 template <typename T, bool kGated, int kOut>
 hipError_t launch_wide(const GroupedArgs& a, hipStream_t s) {
   const int64_t grid = grid_blocks(a, 256, kGated ? 128 : 256);
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (!grid_fits(grid, 512)) return hipErrorInvalidConfiguration;
   wide_kernel<T, kGated, kOut><<<dim3(static_cast<unsigned>(grid)), dim3(512), 0, s>>>(a);
   return hipGetLastError();
 }
@@ -721,7 +721,7 @@ hipError_t launch_wide(const GroupedArgs& a, hipStream_t s) {
 template <typename T, bool kGated, int kOut, int BT, int BC, int WT, int WC, int WK, int S>
 hipError_t launch_tile(const GroupedArgs& a, hipStream_t s) {
   const int64_t grid = grid_blocks(a, BT, kGated ? BC / 2 : BC);
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (!grid_fits(grid, 64 * WT * WC * WK)) return hipErrorInvalidConfiguration;
   tile_kernel<T, kGated, kOut, BT, BC, WT, WC, WK, S>
       <<<dim3(static_cast<unsigned>(grid)), dim3(64 * WT * WC * WK), 0, s>>>(a);
   return hipGetLastError();

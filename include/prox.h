@@ -443,7 +443,8 @@ prox_status prox_proxy_state(const prox_layer* layer, const void* x, int32_t bat
  * Sums, softmax and scales are fp32; a result in a 16-bit type is rounded once,
  * to nearest even.  Results do not depend on the launch: calls with the same
  * arguments give the same bits.  The device must be the current one.  Buffers
- * that a call writes must not overlap the ones it reads.
+ * that a call writes must not overlap the ones it reads.  Strides are at most
+ * 2^40 elements; a launch of 2^32 threads or more gives PROX_ERR_HIP.
  * ---------------------------------------------------------------------------
  */
 
@@ -559,7 +560,7 @@ prox_status prox_fp8_quantize(const void* x, int32_t x_dtype, int32_t rows, int3
  *   weight  device [n_tokens][top_k] fp32
  *   y       device [n_tokens][n] of y_dtype (PROX_F32 or PROX_BF16, overwritten),
  *           rows y_stride elements apart
- * 1 <= top_k <= 32.  Asynchronous.
+ * 1 <= top_k <= 32, n <= 2^24, n_tokens * top_k <= 2^30.  Asynchronous.
  */
 prox_status prox_expert_combine(const void* h, int32_t h_dtype, int32_t h_rows, int64_t h_stride,
                                 const int32_t* row_of, const float* weight, int32_t n_tokens, int32_t top_k, int32_t n,
@@ -567,7 +568,7 @@ prox_status prox_expert_combine(const void* h, int32_t h_dtype, int32_t h_rows, 
 
 /*
  * One routed layer: w_router [n_experts][d_model] (contiguous, 16-byte aligned;
- * PROX_F32 for fp32 layers, PROX_BF16 for bf16 and fp8 ones), up a gated
+ * PROX_F32 for fp32 layers, PROX_BF16 for bf16 and fp8 ones, rows below 8 MiB), up a gated
  * [n_experts][d_ff][d_model], down a plain [n_experts][d_model][d_ff].
  */
 typedef struct {

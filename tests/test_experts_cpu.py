@@ -70,6 +70,39 @@ def test_route_refusals():
     assert P.prox_expert_route_workspace_size(0, 8, 2) % 256 == 0
 
 
+@pytest.mark.parametrize("es,code", [(4, P.PROX_F32), (2, P.PROX_BF16)])
+def test_refuses_strides_beyond_64_bits(es, code):
+    """Strides whose sizes in bytes would pass 64 bits (2^61 fp32 values wrap to
+    a negative stride, which is below every upper limit)."""
+    lib = P.raw_library()
+    for stride in (1 << 61, 1 << 62, (1 << 63) - 16, (1 << 40) + 16):
+        assert _mm(_experts(wdtype=code, row_stride=stride)) == UNSUP
+        assert _mm(_experts(wdtype=code, group_stride=stride)) == UNSUP
+        assert _mm(_experts(wdtype=code), a_stride=stride) == UNSUP
+        assert _mm(_experts(wdtype=code), ostr=stride) == UNSUP
+        assert lib.prox_fp8_quantize(FAKE, code, 4, 128, stride, 1, FAKE, 128, FAKE, None) == UNSUP
+        assert lib.prox_fp8_quantize(FAKE, code, 4, 128, 128, 1, FAKE, stride, FAKE, None) == UNSUP
+        assert lib.prox_expert_combine(FAKE, code, 8, stride, FAKE, FAKE, 4, 2, 64, FAKE, code, 64, None) == UNSUP
+        assert lib.prox_expert_combine(FAKE, code, 8, 64, FAKE, FAKE, 4, 2, 64, FAKE, code, stride, None) == UNSUP
+
+
+def test_combine_refuses_rows_whose_last_index_passes_32_bits():
+    n = (1 << 31) - 1
+    assert P.raw_library().prox_expert_combine(FAKE, P.PROX_BF16, 8, n, FAKE, FAKE, 1, 1, n, FAKE, P.PROX_BF16, n,
+                                               None) == UNSUP
+
+
+def test_moe_refuses_router_rows_of_8_mib():
+    """An fp8 layer's bf16 router has rows twice as wide as its experts'."""
+    lib, size = P.raw_library(), ctypes.c_size_t(0)
+    f8 = dict(wdtype=P.PROX_FP8, w_scale=FAKE)
+    for d, want in (((1 << 22) - 16, P.PROX_OK), (1 << 22, UNSUP)):
+        up = _experts(n=16, k=d, row_stride=d, group_stride=16 * d, w_gate=FAKE, w_gate_scale=FAKE, **f8)
+        down = _experts(n=d, k=16, row_stride=16, group_stride=16 * d, **f8)
+        layer = P.prox_moe_layer(up, down, FAKE, 2, 1, 0)
+        assert lib.prox_moe_workspace_size(ctypes.byref(layer), 4, ctypes.byref(size)) == want
+
+
 def test_quantize_and_combine_refusals():
     lib = P.raw_library()
 
