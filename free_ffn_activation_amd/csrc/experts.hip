@@ -26,26 +26,36 @@ __device__ __forceinline__ float route_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
-// Largest key of the wave, to every lane (DPP row shifts, then row broadcasts; a
-// lane whose source is outside its row reads 0, the smallest key).
-__device__ __forceinline__ uint32_t wave_max_key(uint32_t v) {
-#define PROX_MAX_STEP(ctrl, rows)                                                                     \
-  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), ctrl, rows, 0xF, false)))
-  PROX_MAX_STEP(0x111, 0xF);  // row_shr:1
-  PROX_MAX_STEP(0x112, 0xF);  // row_shr:2
-  PROX_MAX_STEP(0x114, 0xF);  // row_shr:4
-  PROX_MAX_STEP(0x118, 0xF);  // row_shr:8
-  PROX_MAX_STEP(0x142, 0xA);  // row_bcast:15
-  PROX_MAX_STEP(0x143, 0xC);  // row_bcast:31
-#undef PROX_MAX_STEP
-  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+// op over the kLanes neighbouring lanes of a token, to every one of them: rotations
+// inside a row of sixteen, then exchanges of rows and of halves of the wave.  (In
+// every step both partners combine the same two values, so that fp32 sums agree.)
+template <int kLanes, typename Op>
+__device__ __forceinline__ uint32_t token_all(uint32_t v, Op op) {
+#define PROX_ROTATE(n) \
+  v = op(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + n, 0xF, 0xF, false)))
+  PROX_ROTATE(8);
+  PROX_ROTATE(4);
+  PROX_ROTATE(2);
+  PROX_ROTATE(1);
+#undef PROX_ROTATE
+  if constexpr (kLanes >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = op(r[0], r[1]);
+  }
+  if constexpr (kLanes == 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = op(r[0], r[1]);
+  }
+  return v;
 }
 
-constexpr int kRouteThreads = 512;
 constexpr int kPlaceThreads = 1024;
 constexpr int kRouteSub = 64;      // tokens of one bitmap pass: the bits of a word
-constexpr int kRouteSmall = 32;    // tokens of a single-block launch, and of a block of a small launch
+constexpr int kRouteSmall = 32;    // tokens of a block of a small launch
 constexpr int kRouteBlocks = 256;  // blocks at most
+
+// Threads of a block that chooses: for kRouteSmall tokens at once, if a block can.
+__host__ __device__ constexpr int choose_threads(int lanes) { return lanes * kRouteSmall < 1024 ? lanes * kRouteSmall : 1024; }
 
 // Tokens per block: whole passes of kRouteSub beyond kRouteBlocks blocks of
 // kRouteSmall.
@@ -55,84 +65,85 @@ __host__ __device__ inline int route_tokens_per_block(int tokens) {
   return (per + kRouteSub - 1) / kRouteSub * kRouteSub;
 }
 
-// The top_k of kTok tokens (t0, t0 + step, ..) by one wave: kPer logits a lane and
-// token, expert lane + 64 i.  Each round takes the largest key by DPP (no LDS) and,
-// by ballots, the lowest expert that has it.  A round is a chain of dependent
-// instructions, so a wave works on several tokens side by side (8191 tokens of 128
-// experts: four tokens 5.3 us, one 9.2).  id[j]: this lane's slot's expert of token j,
+// The top_k of a token by kLanes lanes, 64 / kLanes tokens a wave: lane l of a token
+// holds the experts l + kLanes i, i < kPer, and its slots l and l + kLanes.  Each round
+// takes the token's largest key, then the lowest expert that has it, by token_all.  A
+// round is a chain of dependent instructions, so what bounds a launch is their number
+// per token (the logits of 8191 x 128 are read in 0.6 us): several tokens share one
+// instruction (both launches, us: 65536 tokens of 128 experts 39.6 against 73 with a
+// wave per token, 8191 of 512 23 against 56).  id: the experts of this lane's slots,
 // or -1.
-template <int kPer, int kTok>
-__device__ __forceinline__ void route_tokens(const RouteArgs& a, int t0, int step, int end, int lane, int (&id)[kTok]) {
-  uint32_t key[kTok][kPer], my_key[kTok];
-  float top[kTok], rest[kTok];  // rest: renormalize 0, the lane's share of the sum over all experts
+template <int kPer, int kLanes>
+__device__ __forceinline__ void route_token(const RouteArgs& a, int t, int end, int lane, int (&id)[2]) {
+  constexpr int kSlots = kLanes < kMaxTopK ? 2 : 1;
+  const auto larger = [](uint32_t x, uint32_t y) { return max(x, y); };
+  const auto smaller = [](uint32_t x, uint32_t y) { return min(x, y); };
+  const auto sum = [](uint32_t x, uint32_t y) { return __float_as_uint(__uint_as_float(x) + __uint_as_float(y)); };
+  uint32_t key[kPer], my_key[2] = {0, 0};
+  // lanes without a logit read another one, so that all loads are under way at once
+  const size_t base = static_cast<size_t>(min(t, end - 1)) * a.experts;
+  float z[kPer];
+  if (a.logits_dtype == PROX_F32) {
 #pragma unroll
-  for (int j = 0; j < kTok; ++j) {
-    const int t = t0 + j * step;
-    const size_t base = static_cast<size_t>(t) * a.experts;
-    uint32_t best = 0;
+    for (int i = 0; i < kPer; ++i) z[i] = load_elem<F32Tag>(a.logits, base + min(lane + kLanes * i, a.experts - 1));
+  } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 64 * i;
-      key[j][i] = 0;
-      if (t < end && e < a.experts)
-        key[j][i] = route_key(a.logits_dtype == PROX_F32 ? load_elem<F32Tag>(a.logits, base + e)
-                                                         : load_elem<Bf16Tag>(a.logits, base + e));
-      best = max(best, key[j][i]);
-    }
-    my_key[j] = best;  // for the loop below
-    id[j] = -1;
+    for (int i = 0; i < kPer; ++i) z[i] = load_elem<Bf16Tag>(a.logits, base + min(lane + kLanes * i, a.experts - 1));
   }
 #pragma unroll
-  for (int j = 0; j < kTok; ++j) {
-    top[j] = route_value(wave_max_key(my_key[j]));
-    my_key[j] = 0;  // lane s holds slot s
-    rest[j] = 0.f;
-    if (!a.renormalize) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (key[j][i] != 0) rest[j] += expf(route_value(key[j][i]) - top[j]);
-    }
-  }
+  for (int i = 0; i < kPer; ++i) key[i] = t < end && lane + kLanes * i < a.experts ? route_key(z[i]) : 0;
+  id[0] = id[1] = -1;
+  float top = 0.f, rest = 0.f;  // rest: renormalize 0, the lane's share of the sum over all experts
   for (int s = 0; s < a.top_k; ++s) {
-    uint32_t best[kTok];
+    uint32_t best = key[0];
 #pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-      best[j] = key[j][0];
+    for (int i = 1; i < kPer; ++i) best = max(best, key[i]);
+    best = token_all<kLanes>(best, larger);
+    if (s == 0) {
+      top = route_value(best);
+      if (!a.renormalize) {
 #pragma unroll
-      for (int i = 1; i < kPer; ++i) best[j] = max(best[j], key[j][i]);
-    }
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) best[j] = wave_max_key(best[j]);
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-      int e = -1;  // best 0: no expert is left
-      if (best[j] != 0) {
-#pragma unroll
-        for (int i = kPer - 1; i >= 0; --i) {
-          const uint64_t has = __ballot(key[j][i] == best[j]);
-          if (has) e = 64 * i + __builtin_ctzll(has);
+        for (int i = 0; i < kPer; ++i) {
+          if (key[i] != 0) rest += expf(route_value(key[i]) - top);
+          __builtin_amdgcn_sched_barrier(0);  // side by side they take all registers
         }
       }
-      if (lane == s) {
-        my_key[j] = best[j];
-        id[j] = e;
+    }
+    uint32_t e = 0xFFFFFFFFu;
+    if constexpr (kLanes == 64) {
+#pragma unroll
+      for (int i = kPer - 1; i >= 0; --i) {
+        const uint64_t has = __ballot(key[i] == best);
+        if (has) e = 64 * i + __builtin_ctzll(has);
       }
+    } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (lane + 64 * i == e) key[j][i] = 0;
+    for (int i = kPer - 1; i >= 0; --i)
+      if (key[i] == best) e = lane + kLanes * i;
+    e = token_all<kLanes>(e, smaller);
     }
-  }
 #pragma unroll
-  for (int j = 0; j < kTok; ++j) {
-    const int t = t0 + j * step;
-    const float p = id[j] >= 0 ? expf(route_value(my_key[j]) - top[j]) : 0.f;
-    const float total = wave_sum(a.renormalize ? p : rest[j]);
-    if (t < end && lane < a.top_k) {
-      const size_t o = static_cast<size_t>(t) * a.top_k + lane;
-      a.expert_idx[o] = id[j];
-      a.weight[o] = id[j] >= 0 ? p / total : 0.f;
-    }
+    for (int i = 0; i < kPer; ++i)
+      if (e == static_cast<uint32_t>(lane + kLanes * i)) key[i] = 0;
+#pragma unroll
+    for (int h = 0; h < kSlots; ++h)
+      if (best != 0 && lane + kLanes * h == s) {  // best 0: no expert is left
+        my_key[h] = best;
+        id[h] = static_cast<int>(e);
+      }
   }
+  float p[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) p[h] = id[h] >= 0 ? expf(route_value(my_key[h]) - top) : 0.f;
+  const float total =
+      __uint_as_float(token_all<kLanes>(__float_as_uint(a.renormalize ? p[0] + p[1] : rest), sum));
+#pragma unroll
+  for (int h = 0; h < kSlots; ++h)
+    if (t < end && lane + kLanes * h < a.top_k) {
+      const size_t o = static_cast<size_t>(t) * a.top_k + lane + kLanes * h;
+      a.expert_idx[o] = id[h];
+      a.weight[o] = id[h] >= 0 ? p[h] / total : 0.f;
+    }
 }
 
 // Exclusive sums of count[0 .. experts) into start, by the whole block; returns
@@ -161,63 +172,70 @@ __device__ __forceinline__ int route_offsets(const int* count, int* start, int e
   return rows;
 }
 
-// Up to kRouteSmall tokens: all in one block.  The chosen experts are kept as one
-// bitmap word per expert (bit = token): a token takes an expert at most once, so
-// its place among the expert's tokens is a population count.
-template <int kPer>
+// Up to kTokens tokens, all in one block.  The chosen experts are kept as one bitmap
+// word per expert (bit = token): a token takes an expert at most once, so its place
+// among the expert's tokens is a population count.
+template <int kPer, int kLanes, int kTokens>
 __global__ void __launch_bounds__(1024) route_small_kernel(RouteArgs a) {
-  __shared__ uint32_t bits[kMaxExperts];
+  typedef typename std::conditional<kTokens <= 32, uint32_t, unsigned long long>::type word_t;
+  __shared__ word_t bits[kMaxExperts];
   __shared__ int count[kMaxExperts], start[kMaxExperts];
   __shared__ int wave_total[16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid % kLanes;
   for (int e = tid; e < a.experts; e += 1024) bits[e] = 0;
   __syncthreads();
-  constexpr int kMine = kRouteSmall / 16;  // tokens of a wave
-  int id[kMine];
-  route_tokens<kPer, kMine>(a, wave, 16, a.tokens, lane, id);
+  constexpr int kAtOnce = 1024 / kLanes, kMine = (kTokens + kAtOnce - 1) / kAtOnce;  // tokens; of a wave's lanes
+  int id[kMine][2];
 #pragma unroll
-  for (int i = 0; i < kMine; ++i)
-    if (id[i] >= 0) atomicOr(&bits[id[i]], 1u << (wave + 16 * i));
+  for (int i = 0; i < kMine; ++i) {
+    const int t = tid / kLanes + kAtOnce * i;
+    id[i][0] = id[i][1] = -1;
+    if (t - (tid & 63) / kLanes < a.tokens) route_token<kPer, kLanes>(a, t, a.tokens, lane, id[i]);  // by whole waves
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (id[i][h] >= 0) atomicOr(&bits[id[i][h]], word_t{1} << t);
+  }
   __syncthreads();
-  for (int e = tid; e < a.experts; e += 1024) count[e] = __popc(bits[e]);
+  for (int e = tid; e < a.experts; e += 1024) count[e] = __popcll(bits[e]);
   __syncthreads();
   const int rows = route_offsets(count, start, a.experts, wave_total);
   for (int e = tid; e < a.experts; e += 1024) a.offsets[e] = start[e];
   if (tid == 0) a.offsets[a.experts] = rows;
 #pragma unroll
-  for (int i = 0; i < kMine; ++i) {
-    const int t = wave + 16 * i;
-    if (t >= a.tokens || lane >= a.top_k) continue;
-    int row = -1;
-    if (id[i] >= 0) {
-      row = start[id[i]] + __popc(bits[id[i]] & ((1u << t) - 1));
-      a.row_token[row] = t;
+  for (int i = 0; i < kMine; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = tid / kLanes + kAtOnce * i, s = lane + kLanes * h, e = id[i][h];
+      if (t >= a.tokens || s >= a.top_k) continue;
+      int row = -1;
+      if (e >= 0) {
+        row = start[e] + __popcll(bits[e] & ((word_t{1} << t) - 1));
+        a.row_token[row] = t;
+      }
+      a.row_of[t * a.top_k + s] = row;
     }
-    a.row_of[t * a.top_k + lane] = row;
-  }
   for (int r = rows + tid; r < a.tokens * a.top_k; r += 1024) a.row_token[r] = -1;
 }
 
 // More tokens, first launch: experts and weights of the block's tokens, and how
 // many rows each expert gets from them.
-template <int kPer>
-__global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(RouteArgs a) {
+template <int kPer, int kLanes>
+__global__ void __launch_bounds__(choose_threads(kLanes)) route_choose_kernel(RouteArgs a) {
+  constexpr int kThreads = choose_threads(kLanes);
   __shared__ int count[kMaxExperts];
   const int per = route_tokens_per_block(a.tokens);
   const int t0 = blockIdx.x * per, t1 = min(a.tokens, t0 + per);
-  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
+  for (int e = threadIdx.x; e < a.experts; e += kThreads) count[e] = 0;
   __syncthreads();
-  const int lane = threadIdx.x & 63;
-  constexpr int kWaves = kRouteThreads / 64, kTok = kPer <= 2 ? 4 : kPer <= 4 ? 2 : 1;
-  for (int t = t0 + (threadIdx.x >> 6); t < t1; t += kWaves * kTok) {
-    int id[kTok];
-    route_tokens<kPer, kTok>(a, t, kWaves, t1, lane, id);
+  for (int t = t0; t < t1; t += kThreads / kLanes) {
+    int id[2];
+    route_token<kPer, kLanes>(a, t + threadIdx.x / kLanes, t1, threadIdx.x % kLanes, id);
 #pragma unroll
-    for (int j = 0; j < kTok; ++j)
-      if (id[j] >= 0) atomicAdd(&count[id[j]], 1);
+    for (int h = 0; h < 2; ++h)
+      if (id[h] >= 0) atomicAdd(&count[id[h]], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads)
+  for (int e = threadIdx.x; e < a.experts; e += kThreads)
     a.block_count[static_cast<size_t>(blockIdx.x) * a.experts + e] = count[e];
 }
 
@@ -514,15 +532,36 @@ size_t route_workspace(int tokens, int experts, int top_k) {
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   const int blocks = route_blocks(a.tokens);
-  const auto per = [&](auto kernel1, auto kernel2, auto kernel4, auto kernel16, int threads) {
-    const auto kernel = a.experts <= 64 ? kernel1 : a.experts <= 128 ? kernel2 : a.experts <= 256 ? kernel4 : kernel16;
+  const auto launch = [&](auto kernel, int threads) {
     kernel<<<dim3(blocks), dim3(threads), 0, s>>>(a);
     return hipGetLastError();
   };
-  if (blocks == 1)
-    return per(route_small_kernel<1>, route_small_kernel<2>, route_small_kernel<4>, route_small_kernel<16>, 1024);
-  const hipError_t e = per(route_choose_kernel<1>, route_choose_kernel<2>, route_choose_kernel<4>,
-                           route_choose_kernel<16>, kRouteThreads);
+  // One block, with as many lanes per token as it has: fewer keys a lane, shorter
+  // rounds.  (us: 1 token of 64 experts 3.9, 64 tokens 6.0, by the two launches 7.7; 64
+  // tokens of 512 experts would take 17.5 in one block, by the two launches 13.6.)
+  if (a.tokens <= 16) {
+    if (a.experts <= 64) return launch(route_small_kernel<1, 64, 16>, 1024);
+    if (a.experts <= 128) return launch(route_small_kernel<2, 64, 16>, 1024);
+    if (a.experts <= 256) return launch(route_small_kernel<4, 64, 16>, 1024);
+    if (a.experts <= 512) return launch(route_small_kernel<8, 64, 16>, 1024);
+    return launch(route_small_kernel<16, 64, 16>, 1024);
+  }
+  if (a.tokens <= 64 && a.experts <= 128)
+    return a.experts <= 64 ? launch(route_small_kernel<4, 16, 64>, 1024) : launch(route_small_kernel<8, 16, 64>, 1024);
+  if (a.tokens <= 32) {
+    if (a.experts <= 256) return launch(route_small_kernel<8, 32, 32>, 1024);
+    if (a.experts <= 512) return launch(route_small_kernel<16, 32, 32>, 1024);
+    return launch(route_small_kernel<16, 64, 32>, 1024);
+  }
+  // Two launches; a block has all its tokens at once where it can.  (us, tokens x
+  // experts, keys by lanes per token: 65536 x 64: 4 x 16 25.6, 2 x 32 29.0; 65536 x 128:
+  // 4 x 32 39.6, 8 x 16 50.9; 16384 x 256: 8 x 32 21.5, 4 x 64 26.9; 65536 x 512: 16 x 32
+  // 81, 8 x 64 100; 8191 x 1024: 16 x 64 41.5, 32 x 32 43.0)
+  const hipError_t e = a.experts <= 64    ? launch(route_choose_kernel<4, 16>, choose_threads(16))
+                       : a.experts <= 128 ? launch(route_choose_kernel<4, 32>, choose_threads(32))
+                       : a.experts <= 256 ? launch(route_choose_kernel<8, 32>, choose_threads(32))
+                       : a.experts <= 512 ? launch(route_choose_kernel<16, 32>, choose_threads(32))
+                                          : launch(route_choose_kernel<16, 64>, choose_threads(64));
   if (e != hipSuccess) return e;
   route_place_kernel<<<dim3(blocks), dim3(kPlaceThreads), 0, s>>>(a, blocks);
   return hipGetLastError();

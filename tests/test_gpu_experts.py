@@ -332,6 +332,19 @@ def test_route(t, e, k, dtype):
     check_route(gen(t + e).standard_normal((t, e)) * 2, k, renorm=t % 2 == 1, dtype=dtype)
 
 
+@pytest.mark.parametrize("e", [63, 64, 65, 128, 129, 256, 257, 512, 513, 1024])
+def test_route_at_the_sizes_where_launches_change(e):
+    """Numbers of tokens on both sides of the one-block launches' limits, with one
+    slot, several, and the most; a token without experts and one of equal logits."""
+    for t in (1, 15, 16, 17, 31, 32, 33, 63, 64, 65):
+        z = gen(17 * t + e).standard_normal((t, e)) * 3
+        z[t // 2] = -np.inf
+        z[t - 1] = 1.5
+        for k in (1, 5, 32):
+            check_route(z, k, renorm=(t + k) % 2 == 1, dtype="bf16" if k == 5 else "f32")
+
+
+
 @pytest.mark.parametrize("t,e,k", [(1, 16, 4), (50, 64, 8), (300, 40, 8)])
 def test_route_masks_and_ties(t, e, k):
     r = gen(e)
