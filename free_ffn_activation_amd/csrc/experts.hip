@@ -53,6 +53,10 @@ constexpr int kPlaceThreads = 1024;
 constexpr int kRouteSub = 64;      // tokens of one bitmap pass: the bits of a word
 constexpr int kRouteSmall = 32;    // tokens of a block of a small launch
 constexpr int kRouteBlocks = 256;  // blocks at most
+static_assert(kRouteSmall * kRouteBlocks < 1 << 16, "sums of byte counts are kept two to a word");
+
+// Bytes of a block's counts where each is one byte.
+__host__ __device__ inline int byte_counts(int experts) { return (experts + 3) / 4 * 4; }
 
 // Threads of a block that chooses: for kRouteSmall tokens at once, if a block can.
 __host__ __device__ constexpr int choose_threads(int lanes) { return lanes * kRouteSmall < 1024 ? lanes * kRouteSmall : 1024; }
@@ -235,72 +239,134 @@ __global__ void __launch_bounds__(choose_threads(kLanes)) route_choose_kernel(Ro
       if (id[h] >= 0) atomicAdd(&count[id[h]], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.experts; e += kThreads)
-    a.block_count[static_cast<size_t>(blockIdx.x) * a.experts + e] = count[e];
+  if (per == kRouteSmall) {
+    const int bytes = byte_counts(a.experts);
+    uint8_t* p = reinterpret_cast<uint8_t*>(a.block_count) + static_cast<size_t>(blockIdx.x) * bytes;
+    for (int e = threadIdx.x; e < bytes; e += kThreads) p[e] = static_cast<uint8_t>(e < a.experts ? count[e] : 0);
+  } else {
+    int* p = a.block_count + static_cast<size_t>(blockIdx.x) * a.experts;
+    for (int e = threadIdx.x; e < a.experts; e += kThreads) p[e] = count[e];
+  }
 }
 
 // Second launch: every block adds up the counts of all blocks (so that no block
-// waits for another), then places its own rows.  The counts are read by all
-// threads, kPlaceThreads / experts blocks' rows side by side.
+// waits for another), then places its own rows.  What bounds it is a chain of
+// latencies: its own experts are read first, and the counts by all threads side by
+// side; in blocks of kRouteSmall tokens they are bytes, four to a load, whose sums
+// (kRouteSmall * kRouteBlocks at most) are kept two to a word.
+template <bool kBytes>
 __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(RouteArgs a, int blocks) {
-  __shared__ int next[kMaxExperts];   // rows of earlier blocks, then the next row of each expert
-  __shared__ int total[kMaxExperts];
+  __shared__ uint32_t next[kMaxExperts];   // rows of earlier blocks, then the next row of each expert
+  __shared__ uint32_t total[kMaxExperts];
+  __shared__ int start[kMaxExperts];
   __shared__ unsigned long long bits[kMaxExperts];
   __shared__ int wave_total[kPlaceThreads / 64];
+  constexpr int kMine = kRouteSub * kMaxTopK / kPlaceThreads;  // slots of a thread in a pass
   const int tid = threadIdx.x, me = blockIdx.x;
-  for (int e = tid; e < a.experts; e += kPlaceThreads) next[e] = total[e] = 0;
+  const int tpb = route_tokens_per_block(a.tokens);
+  const int t0 = me * tpb, t1 = min(a.tokens, t0 + tpb);
+  int mine[kMine];  // their experts, or -1
+  const auto read = [&](int s0) {
+    const int slots = min(kRouteSub, t1 - s0) * a.top_k;
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int i = tid + u * kPlaceThreads;
+      mine[u] = i < slots ? a.expert_idx[static_cast<size_t>(s0) * a.top_k + i] : -1;
+    }
+  };
+  const auto mark = [&] {
+#pragma unroll
+    for (int u = 0; u < kMine; ++u)
+      if (mine[u] >= 0) atomicOr(&bits[mine[u]], 1ull << ((tid + u * kPlaceThreads) / a.top_k));
+  };
+  read(t0);
+  for (int e = tid; e < kMaxExperts; e += kPlaceThreads) {
+    next[e] = total[e] = 0;
+    bits[e] = 0;
+  }
   __syncthreads();
-  {
-    const int side = max(1, kPlaceThreads / a.experts);  // blocks' rows read side by side
-    const int lane_block = tid / a.experts;
-    for (int e0 = 0; e0 < a.experts; e0 += kPlaceThreads) {  // one pass up to kPlaceThreads experts
-      const int e = e0 + (side > 1 || a.experts == kPlaceThreads ? tid % a.experts : tid);
-      if (e >= a.experts || (side > 1 && lane_block >= side)) continue;
-      const int* p = a.block_count + e;
-      int before = 0, sum = 0;
+  // columns: experts, or fours of them; `side` blocks' counts are read side by side
+  const int columns = kBytes ? byte_counts(a.experts) / 4 : a.experts;
+  const int side = kPlaceThreads / columns, column = tid % columns;
+  if (tid < side * columns) {
+    if constexpr (kBytes) {
+      uint32_t before[2] = {0, 0}, sum[2] = {0, 0};  // experts 0 and 2, 1 and 3 of the four
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.block_count) + column;
+#pragma unroll 8
+      for (int b = tid / columns; b < blocks; b += side) {
+        const uint32_t c = p[static_cast<size_t>(b) * columns];
+        const uint32_t c0 = c & 0x00FF00FFu, c1 = c >> 8 & 0x00FF00FFu;
+        sum[0] += c0;
+        sum[1] += c1;
+        before[0] += b < me ? c0 : 0;
+        before[1] += b < me ? c1 : 0;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        atomicAdd(&next[2 * column + h], before[h]);
+        atomicAdd(&total[2 * column + h], sum[h]);
+      }
+    } else {
+      uint32_t before = 0, sum = 0;
+      const int* p = a.block_count + column;
 #pragma unroll 16
-      for (int b = side > 1 ? lane_block : 0; b < blocks; b += side) {
-        const int c = p[static_cast<size_t>(b) * a.experts];
+      for (int b = tid / columns; b < blocks; b += side) {
+        const uint32_t c = p[static_cast<size_t>(b) * columns];
         before += b < me ? c : 0;
         sum += c;
       }
-      atomicAdd(&next[e], before);
-      atomicAdd(&total[e], sum);
+      atomicAdd(&next[column], before);
+      atomicAdd(&total[column], sum);
     }
   }
+  mark();
   __syncthreads();
-  int* start = reinterpret_cast<int*>(bits);
-  const int rows = route_offsets(total, start, a.experts, wave_total);
+  if constexpr (kBytes) {  // to a word per expert
+    uint32_t n = 0, m = 0;
+    const int word = tid / 4 * 2 + (tid & 1), shift = (tid & 2) * 8;
+    if (tid < a.experts) {
+      n = next[word] >> shift & 0xFFFFu;
+      m = total[word] >> shift & 0xFFFFu;
+    }
+    __syncthreads();
+    if (tid < a.experts) {
+      next[tid] = n;
+      total[tid] = m;
+    }
+    __syncthreads();
+  }
+  const int rows = route_offsets(reinterpret_cast<const int*>(total), start, a.experts, wave_total);
   for (int e = tid; e < a.experts; e += kPlaceThreads) {
     if (me == 0) a.offsets[e] = start[e];
     next[e] += start[e];
   }
   if (me == 0 && tid == 0) a.offsets[a.experts] = rows;
-  const int tpb = route_tokens_per_block(a.tokens);
-  const int t0 = me * tpb, t1 = min(a.tokens, t0 + tpb);
+  __syncthreads();
   for (int s0 = t0; s0 < t1; s0 += kRouteSub) {
-    const int nt = min(kRouteSub, t1 - s0);
-    __syncthreads();
-    for (int e = tid; e < a.experts; e += kPlaceThreads) bits[e] = 0;
-    __syncthreads();
-    for (int i = tid; i < nt * a.top_k; i += kPlaceThreads) {
-      const int e = a.expert_idx[static_cast<size_t>(s0) * a.top_k + i];
-      if (e >= 0) atomicOr(&bits[e], 1ull << (i / a.top_k));
+    if (s0 > t0) {
+      read(s0);
+      __syncthreads();
+      for (int e = tid; e < a.experts; e += kPlaceThreads) {
+        next[e] += __popcll(bits[e]);
+        bits[e] = 0;
+      }
+      __syncthreads();
+      mark();
+      __syncthreads();
     }
-    __syncthreads();
-    for (int i = tid; i < nt * a.top_k; i += kPlaceThreads) {
-      const int t = i / a.top_k;
-      const size_t o = static_cast<size_t>(s0) * a.top_k + i;
-      const int e = a.expert_idx[o];
+    const int slots = min(kRouteSub, t1 - s0) * a.top_k;
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int i = tid + u * kPlaceThreads;
+      if (i >= slots) continue;
+      const int t = i / a.top_k, e = mine[u];
       int row = -1;
       if (e >= 0) {
-        row = next[e] + __popcll(bits[e] & ((1ull << t) - 1));
+        row = static_cast<int>(next[e]) + __popcll(bits[e] & ((1ull << t) - 1));
         a.row_token[row] = s0 + t;
       }
-      a.row_of[o] = row;
+      a.row_of[static_cast<size_t>(s0) * a.top_k + i] = row;
     }
-    __syncthreads();
-    for (int e = tid; e < a.experts; e += kPlaceThreads) next[e] += __popcll(bits[e]);
   }
   // rows behind the last expert's
   const int all = a.tokens * a.top_k;
@@ -563,7 +629,10 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
                        : a.experts <= 512 ? launch(route_choose_kernel<16, 32>, choose_threads(32))
                                           : launch(route_choose_kernel<16, 64>, choose_threads(64));
   if (e != hipSuccess) return e;
-  route_place_kernel<<<dim3(blocks), dim3(kPlaceThreads), 0, s>>>(a, blocks);
+  if (route_tokens_per_block(a.tokens) == kRouteSmall)
+    route_place_kernel<true><<<dim3(blocks), dim3(kPlaceThreads), 0, s>>>(a, blocks);
+  else
+    route_place_kernel<false><<<dim3(blocks), dim3(kPlaceThreads), 0, s>>>(a, blocks);
   return hipGetLastError();
 }
 
