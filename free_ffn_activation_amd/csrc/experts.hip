@@ -59,7 +59,9 @@ static_assert(kRouteSmall * kRouteBlocks < 1 << 16, "sums of byte counts are kep
 __host__ __device__ inline int byte_counts(int experts) { return (experts + 3) / 4 * 4; }
 
 // Threads of a block that chooses: for kRouteSmall tokens at once, if a block can.
-__host__ __device__ constexpr int choose_threads(int lanes) { return lanes * kRouteSmall < 1024 ? lanes * kRouteSmall : 1024; }
+__host__ __device__ constexpr int choose_threads(int lanes) {
+  return lanes * kRouteSmall < 1024 ? lanes * kRouteSmall : 1024;
+}
 
 // Tokens per block: whole passes of kRouteSub beyond kRouteBlocks blocks of
 // kRouteSmall.
@@ -73,10 +75,11 @@ __host__ __device__ inline int route_tokens_per_block(int tokens) {
 // holds the experts l + kLanes i, i < kPer, and its slots l and l + kLanes.  Each round
 // takes the token's largest key, then the lowest expert that has it, by token_all.  A
 // round is a chain of dependent instructions, so what bounds a launch is their number
-// per token (the logits of 8191 x 128 are read in 0.6 us): several tokens share one
-// instruction (both launches, us: 65536 tokens of 128 experts 39.6 against 73 with a
-// wave per token, 8191 of 512 23 against 56).  id: the experts of this lane's slots,
-// or -1.
+// per token (the logits of 8191 x 128 are read in 0.6 us, the launch takes 6): several
+// tokens share one instruction (with the same second launch, us: 65536 tokens of 128
+// experts 39.6, a wave per token 73; 8191 of 512 23 and 56).  A whole wave finds the
+// lowest expert by ballots, which are shorter than its second reduction (1024 experts:
+// 77 and 82).  id: the experts of this lane's slots, or -1.
 template <int kPer, int kLanes>
 __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int end, int lane, int (&id)[2]) {
   constexpr int kSlots = kLanes < kMaxTopK ? 2 : 1;
@@ -122,9 +125,9 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int end, 
       }
     } else {
 #pragma unroll
-    for (int i = kPer - 1; i >= 0; --i)
-      if (key[i] == best) e = lane + kLanes * i;
-    e = token_all<kLanes>(e, smaller);
+      for (int i = kPer - 1; i >= 0; --i)
+        if (key[i] == best) e = lane + kLanes * i;
+      e = token_all<kLanes>(e, smaller);
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
@@ -253,7 +256,8 @@ __global__ void __launch_bounds__(choose_threads(kLanes)) route_choose_kernel(Ro
 // waits for another), then places its own rows.  What bounds it is a chain of
 // latencies: its own experts are read first, and the counts by all threads side by
 // side; in blocks of kRouteSmall tokens they are bytes, four to a load, whose sums
-// (kRouteSmall * kRouteBlocks at most) are kept two to a word.
+// (kRouteSmall * kRouteBlocks at most) are kept two to a word.  (8191 tokens of 128
+// experts: 5.5 us; with counts of 32 bits, its experts read after them, 7.0.)
 template <bool kBytes>
 __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(RouteArgs a, int blocks) {
   __shared__ uint32_t next[kMaxExperts];   // rows of earlier blocks, then the next row of each expert

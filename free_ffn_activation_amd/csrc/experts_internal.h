@@ -43,7 +43,7 @@ struct RouteArgs {
   int* offsets;        // [experts + 1]
   int* row_token;      // [tokens * top_k]
   int* row_of;         // [tokens][top_k]
-  int* block_count;    // workspace: [blocks][experts]
+  int* block_count;    // workspace: rows of each expert by block, int32 or bytes
 };
 size_t route_workspace(int tokens, int experts, int top_k);
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);

@@ -524,7 +524,8 @@ prox_status prox_grouped_matmul(const prox_experts* experts, const void* a, int3
  *                behind the last row
  *   row_of       device [n_tokens][top_k] int32: the row of each slot, or -1
  *   ws           device, >= prox_expert_route_workspace_size bytes, 256-byte
- *                aligned, no zeroing needed
+ *                aligned, no zeroing needed (calls that overlap in time need
+ *                workspaces of their own)
  * 1 <= top_k <= min(n_experts, 32), n_experts <= 1024, n_tokens * top_k <= 2^30;
  * n_tokens 0 gives zero offsets.  Asynchronous.
  */
