@@ -332,6 +332,33 @@ def test_route(t, e, k, dtype):
     check_route(gen(t + e).standard_normal((t, e)) * 2, k, renorm=t % 2 == 1, dtype=dtype)
 
 
+@pytest.mark.parametrize("t,e,k", [(5, 64, 4), (61, 128, 8), (1000, 200, 6), (8193, 40, 3)])
+def test_route_captured_and_replayed(t, e, k):
+    """Replays with new logits, over a workspace that others have written to."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    logits = torch.zeros(t, e, device="cuda")
+    out = [torch.empty(t, k, **i32), torch.empty(t, k, device="cuda"), torch.empty(e + 1, **i32),
+           torch.empty(t * k, **i32), torch.empty(t, k, **i32)]
+    ws = torch.empty(P.prox_expert_route_workspace_size(t, e, k), dtype=torch.uint8, device="cuda")
+    P.prox_expert_route(logits, *out, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        P.prox_expert_route(logits, *out, ws)
+    for n in range(3):
+        z = gen(n + t).standard_normal((t, e)).astype(np.float32)
+        want = route(z, k)[1]
+        for v in out:
+            v.fill_(77)
+        ws.fill_(200 + n)
+        logits.copy_(torch.from_numpy(z))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for name, v in zip(("idx", "weight", "offsets", "row_token", "row_of"), out):
+            assert np.array_equal(v.cpu().numpy(), want[name]), name
+
+
 @pytest.mark.parametrize("e", [63, 64, 65, 128, 129, 256, 257, 512, 513, 1024])
 def test_route_at_the_sizes_where_launches_change(e):
     """Numbers of tokens on both sides of the one-block launches' limits, with one
