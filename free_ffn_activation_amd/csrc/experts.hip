@@ -419,11 +419,15 @@ __device__ __forceinline__ float block_scale(uint32_t amax) {
 // against the 10 and more of a division, 20 against 26 us for 8192 x 4096 values.
 // Remainders must not underflow: below 2^-80 (a block of values that small) plain
 // divisions.  Quotients so small that theirs do are codes of 0 either way.
+// A scale of a few subnormal steps is rounded down by up to a third, so that
+// quotients reach 672: they are held at the largest code, 448, since the conversion
+// makes NaN of anything above 464.  Scales of 2^-136 and more are off by 2^-14 at
+// most, and their quotients round to 448 by themselves.
 template <int N>
 __device__ __forceinline__ void divide(const float (&v)[N], float scale, float (&q)[N]) {
   if (scale < 0x1p-80f) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) q[i] = scale == 0.f ? 0.f : v[i] / scale;
+    for (int i = 0; i < N; ++i) q[i] = scale == 0.f ? 0.f : fminf(fmaxf(v[i] / scale, -448.f), 448.f);
     return;
   }
   const float inv = 1.0f / scale;

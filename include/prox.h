@@ -537,9 +537,10 @@ prox_status prox_expert_route(const void* logits, int32_t logits_dtype, int32_t 
 /*
  * Quantizer to e4m3 with one fp32 scale per block of block_rows x 128 values:
  *   scale = fp32(amax / 448), amax the block's largest |x|
- *   q     = e4m3(fp32(x / scale)), to nearest, ties to even
- * An all-zero block has scale 0 and codes 0; a block that holds an infinity or
- * NaN has scale NaN and codes NaN.
+ *   q     = e4m3(fp32(x / scale)), to nearest, ties to even, at most +-448
+ *           (larger quotients arise where the scale is a few subnormal steps)
+ * A block whose scale is 0 (all zeros, or values below 2^-141) has codes 0; a
+ * block that holds an infinity or NaN has scale NaN and codes NaN.
  *   x           device [rows][k], PROX_F32 or PROX_BF16, rows x_stride elements
  *               apart; x and its rows 16-byte aligned, k a multiple of 16
  *   block_rows  1 (activations) or 128 (weights; the last block may have fewer

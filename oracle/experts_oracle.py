@@ -52,7 +52,8 @@ def round_e4m3(v: np.ndarray) -> np.ndarray:
 
 def quantize(x: np.ndarray, block_rows: int):
     """(values of the codes, scales): scale = fp32(amax / 448), code =
-    e4m3(fp32(x / scale)), per block_rows x 128 block of fp32 x."""
+    e4m3(fp32(x / scale)) within +-448, per block_rows x 128 block of fp32 x.
+    (A scale of a few subnormal steps may be rounded down by up to a third.)"""
     x = np.asarray(x, np.float32)
     R, K = x.shape
     scale = np.zeros((-(-R // block_rows), -(-K // 128)), np.float32)
@@ -66,7 +67,7 @@ def quantize(x: np.ndarray, block_rows: int):
                 continue
             scale[i, j] = amax / np.float32(448.0)
             if scale[i, j] > 0:
-                q[b] = round_e4m3((x[b] / scale[i, j]).astype(np.float64))
+                q[b] = round_e4m3(np.clip(x[b] / scale[i, j], -448.0, 448.0).astype(np.float64))
     return q, scale
 
 
