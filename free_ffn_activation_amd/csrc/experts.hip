@@ -605,37 +605,38 @@ size_t route_workspace(int tokens, int experts, int top_k) {
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
-  const int blocks = route_blocks(a.tokens);
-  const auto launch = [&](auto kernel, int threads) {
+  const auto launch = [&](auto kernel, int blocks, int threads) {
     kernel<<<dim3(blocks), dim3(threads), 0, s>>>(a);
     return hipGetLastError();
   };
+  const auto launch_small = [&](auto kernel) { return launch(kernel, 1, 1024); };
   // One block, with as many lanes per token as it has: fewer keys a lane, shorter
-  // rounds.  (us: 1 token of 64 experts 3.9, 64 tokens 6.0, by the two launches 7.7; 64
+  // rounds.  (us: 1 token of 64 experts 3.5, 64 tokens 5.6, 65 by the two launches 7.5; 64
   // tokens of 512 experts would take 17.5 in one block, by the two launches 13.6.)
   if (a.tokens <= 16) {
-    if (a.experts <= 64) return launch(route_small_kernel<1, 64, 16>, 1024);
-    if (a.experts <= 128) return launch(route_small_kernel<2, 64, 16>, 1024);
-    if (a.experts <= 256) return launch(route_small_kernel<4, 64, 16>, 1024);
-    if (a.experts <= 512) return launch(route_small_kernel<8, 64, 16>, 1024);
-    return launch(route_small_kernel<16, 64, 16>, 1024);
+    if (a.experts <= 64) return launch_small(route_small_kernel<1, 64, 16>);
+    if (a.experts <= 128) return launch_small(route_small_kernel<2, 64, 16>);
+    if (a.experts <= 256) return launch_small(route_small_kernel<4, 64, 16>);
+    if (a.experts <= 512) return launch_small(route_small_kernel<8, 64, 16>);
+    return launch_small(route_small_kernel<16, 64, 16>);
   }
   if (a.tokens <= 64 && a.experts <= 128)
-    return a.experts <= 64 ? launch(route_small_kernel<4, 16, 64>, 1024) : launch(route_small_kernel<8, 16, 64>, 1024);
+    return a.experts <= 64 ? launch_small(route_small_kernel<4, 16, 64>) : launch_small(route_small_kernel<8, 16, 64>);
   if (a.tokens <= 32) {
-    if (a.experts <= 256) return launch(route_small_kernel<8, 32, 32>, 1024);
-    if (a.experts <= 512) return launch(route_small_kernel<16, 32, 32>, 1024);
-    return launch(route_small_kernel<16, 64, 32>, 1024);
+    if (a.experts <= 256) return launch_small(route_small_kernel<8, 32, 32>);
+    if (a.experts <= 512) return launch_small(route_small_kernel<16, 32, 32>);
+    return launch_small(route_small_kernel<16, 64, 32>);
   }
   // Two launches; a block has all its tokens at once where it can.  (us, tokens x
   // experts, keys by lanes per token: 65536 x 64: 4 x 16 25.6, 2 x 32 29.0; 65536 x 128:
   // 4 x 32 39.6, 8 x 16 50.9; 16384 x 256: 8 x 32 21.5, 4 x 64 26.9; 65536 x 512: 16 x 32
   // 81, 8 x 64 100; 8191 x 1024: 16 x 64 41.5, 32 x 32 43.0)
-  const hipError_t e = a.experts <= 64    ? launch(route_choose_kernel<4, 16>, choose_threads(16))
-                       : a.experts <= 128 ? launch(route_choose_kernel<4, 32>, choose_threads(32))
-                       : a.experts <= 256 ? launch(route_choose_kernel<8, 32>, choose_threads(32))
-                       : a.experts <= 512 ? launch(route_choose_kernel<16, 32>, choose_threads(32))
-                                          : launch(route_choose_kernel<16, 64>, choose_threads(64));
+  const int blocks = route_blocks(a.tokens);
+  const hipError_t e = a.experts <= 64    ? launch(route_choose_kernel<4, 16>, blocks, choose_threads(16))
+                       : a.experts <= 128 ? launch(route_choose_kernel<4, 32>, blocks, choose_threads(32))
+                       : a.experts <= 256 ? launch(route_choose_kernel<8, 32>, blocks, choose_threads(32))
+                       : a.experts <= 512 ? launch(route_choose_kernel<16, 32>, blocks, choose_threads(32))
+                                          : launch(route_choose_kernel<16, 64>, blocks, choose_threads(64));
   if (e != hipSuccess) return e;
   if (route_tokens_per_block(a.tokens) == kRouteSmall)
     route_place_kernel<true><<<dim3(blocks), dim3(kPlaceThreads), 0, s>>>(a, blocks);

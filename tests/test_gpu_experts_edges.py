@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from launches import launches
 from oracle import experts_oracle as O
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +36,22 @@ def test_quantize_where_the_scale_is_a_few_subnormal_steps(block_rows):
     assert not np.isnan(got).any()
     assert np.array_equal(got, rq)
     assert abs(rq).max() == 448
+
+
+# ------------------------------------------------------------------ router
+@pytest.mark.parametrize("e", [5, 64, 65, 128])
+def test_route_in_one_launch_is_one_block(e):
+    """One block takes all tokens of such a call: a second one would do the same
+    work again and write every output a second time, unordered."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for t in (1, 16, 17, 32, 33, 47, 63, 64, 65):
+        k = min(e, 8)
+        bufs = (torch.zeros(t, e, device="cuda"), torch.empty(t, k, **i32), torch.empty(t, k, device="cuda"),
+                torch.empty(e + 1, **i32), torch.empty(t * k, **i32), torch.empty(t, k, **i32),
+                torch.empty(P.prox_expert_route_workspace_size(t, e, k), dtype=torch.uint8, device="cuda"))
+        found = launches(lambda s: P.prox_expert_route(*bufs, stream=s))
+        if t <= 64:
+            assert len(found) == 1 and found[0][1] == 1, (t, found)
+            assert "route_small_kernel" in found[0][0], found
+        else:
+            assert [f[1] for f in found] == [3, 3], (t, found)
