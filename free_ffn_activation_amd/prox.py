@@ -482,6 +482,14 @@ def prox_set_wait_limit(ticks: int) -> int:
 _EXPERT_TYPES = {torch.float32: PROX_F32, torch.bfloat16: PROX_BF16, torch.float8_e4m3fn: PROX_FP8}
 _OUT_TYPES = {torch.float32: PROX_F32, torch.bfloat16: PROX_BF16}
 _I32, _FLOAT = torch.int32, torch.float32
+_MAX = 0x7FFFFFFF
+
+
+def _int32(*values: int) -> None:
+    """Refuses sizes that ctypes would cut to their low 32 bits."""
+    for v in values:
+        if not -_MAX <= v <= _MAX:
+            raise ValueError(f"a size of {v} does not fit 32 bits")
 
 
 def _no_type(t: torch.Tensor, types: dict, name: str) -> TypeError:
@@ -494,6 +502,8 @@ def _matrix(t: torch.Tensor, name: str) -> tuple:
     if len(shape) != 2:
         raise ValueError(f"{name} must have two dimensions, not {len(shape)}")
     rows, cols = shape
+    if rows > _MAX or cols > _MAX:
+        _int32(rows, cols)
     if t.is_contiguous() or rows <= 1 and (cols <= 1 or t.stride(1) == 1):
         return rows, cols, cols  # the stride of a single row is not used
     s0, s1 = t.stride()
@@ -550,6 +560,7 @@ class ProxExperts:
         if w.dim() != 3:
             raise ValueError("w must be [n_groups, n, k]")
         self.n_groups, self.n, self.k = (int(v) for v in w.shape)
+        _int32(self.n_groups, self.n, self.k, activation)
         if w.dtype not in _EXPERT_TYPES:
             raise _no_type(w, _EXPERT_TYPES, "w")
         self.wdtype, self.dtype = _EXPERT_TYPES[w.dtype], w.dtype
@@ -606,6 +617,7 @@ def prox_grouped_matmul(experts: ProxExperts, a: torch.Tensor, out: torch.Tensor
 
 
 def prox_expert_route_workspace_size(n_tokens: int, n_experts: int, top_k: int) -> int:
+    _int32(n_tokens, n_experts, top_k)
     out = _c_size()
     _check(_lib.prox_expert_route_workspace_size(n_tokens, n_experts, top_k, ctypes.byref(out)))
     return int(out.value)
@@ -621,6 +633,8 @@ def prox_expert_route(logits: torch.Tensor, expert_idx: torch.Tensor, weight: to
         raise ValueError("logits must be contiguous [tokens, experts], expert_idx [tokens, top_k]")
     t, e = logits.shape
     k = shape[1]
+    if t > _MAX or e > _MAX or k > _MAX:
+        _int32(t, e, k)
     logits_type = _OUT_TYPES.get(logits.dtype)
     if logits_type is None:
         raise _no_type(logits, _OUT_TYPES, "logits")
@@ -655,6 +669,8 @@ def prox_expert_combine(h: torch.Tensor, row_of: torch.Tensor, weight: torch.Ten
     if len(shape) != 2 or shape[0] != t or y_n != n:
         raise ValueError("row_of must be [tokens, top_k] and y [tokens, columns of h]")
     k = shape[1]
+    if k > _MAX:
+        _int32(k)
     h_type, y_type = _OUT_TYPES.get(h.dtype), _OUT_TYPES.get(y.dtype)
     if h_type is None or y_type is None:
         raise _no_type(h if h_type is None else y, _OUT_TYPES, "h" if h_type is None else "y")
@@ -670,6 +686,7 @@ class ProxMoeLayer:
     def __init__(self, w_router: torch.Tensor, up: ProxExperts, down: ProxExperts, top_k: int, renormalize: bool = True):
         want = torch.float32 if up.wdtype == PROX_F32 else torch.bfloat16
         _flat(w_router, (up.n_groups, up.k), want, "w_router")
+        _int32(top_k)
         if up.device != w_router.device or down.device != w_router.device:
             raise ValueError("the layer's weights are on different devices")
         self.w_router, self.up, self.down, self.top_k = w_router, up, down, top_k
@@ -680,6 +697,7 @@ class ProxMoeLayer:
 
 
 def prox_moe_workspace_size(layer: ProxMoeLayer, n_tokens: int) -> int:
+    _int32(n_tokens)
     out = _c_size()
     _check(_lib.prox_moe_workspace_size(ctypes.byref(layer.desc), n_tokens, ctypes.byref(out)))
     return int(out.value)
@@ -690,6 +708,7 @@ def prox_moe_ffn(layer: ProxMoeLayer, x: torch.Tensor, y: torch.Tensor, ws: torc
     if x.dim() != 2:
         raise ValueError("x must be [tokens, d_model]")
     shape = (x.shape[0], layer.up.k)
+    _int32(shape[0])
     _launch(_lib.prox_moe_ffn, _device_of(layer.w_router, x, y, ws), stream, layer._ref,
             _flat(x, shape, layer.x_dtype, "x"), shape[0], _flat(y, shape, _FLOAT, "y"), _ptr(ws),
             ws.numel() * ws.element_size())

@@ -2,6 +2,7 @@
 (no GPU needed)."""
 import numpy as np
 import pytest
+import torch
 
 from oracle import experts_oracle as O
 
@@ -16,3 +17,56 @@ def test_oracle_holds_quotients_at_the_largest_code():
     q, s = O.quantize(x, 1)
     assert s[0, 0] == np.float32(2.0 ** -149)
     assert q[0, :4].tolist() == [448, -448, 208, 1]
+
+
+# ------------------------------------------------- sizes that do not fit 32 bits
+WIDE = 1 << 32  # a size of WIDE + 2 would reach the library as 2
+
+
+def _layer(**kw):
+    w = [torch.zeros(s, dtype=torch.bfloat16) for s in ((4, 32, 64), (4, 32, 64), (4, 64, 32), (4, 64))]
+    args = dict(top_k=2)
+    args.update(kw)
+    return P.ProxMoeLayer(w[3], P.ProxExperts(w[0], w[1]), P.ProxExperts(w[2]), **args)
+
+
+def test_binding_refuses_counts_beyond_32_bits():
+    for args in ((WIDE + 4, 8, 2), (4, WIDE + 8, 2), (4, 8, WIDE + 2), (-WIDE + 4, 8, 2)):
+        with pytest.raises(ValueError, match="32 bits"):
+            P.prox_expert_route_workspace_size(*args)
+    layer = _layer()
+    assert P.prox_moe_workspace_size(layer, 2) > 0
+    with pytest.raises(ValueError, match="32 bits"):
+        P.prox_moe_workspace_size(layer, WIDE + 2)
+    for kw in (dict(top_k=WIDE + 2), dict(top_k=2 - WIDE)):
+        with pytest.raises(ValueError, match="32 bits"):
+            _layer(**kw)
+
+
+def test_binding_refuses_tensors_beyond_32_bits():
+    def meta(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device="meta")
+    one = torch.zeros(1, 16, 32, dtype=torch.bfloat16)
+    i32, f32, f8 = torch.int32, torch.float32, torch.float8_e4m3fn
+    e = P.ProxExperts(one)
+    many = WIDE + 2
+    for call in (
+            lambda: P.ProxExperts(one.expand(many, 16, 32)),
+            lambda: P.ProxExperts(meta(1, many, 32)),
+            lambda: P.ProxExperts(one, activation=WIDE),
+            lambda: P.prox_grouped_matmul(e, meta(4, 32), meta(many, 16), row_index=meta(many, dtype=i32)),
+            lambda: P.prox_grouped_matmul(e, meta(many, 32), meta(4, 16)),
+            lambda: P.prox_fp8_quantize(meta(many, 16), meta(many, 16, dtype=f8), meta(many, 1, dtype=f32)),
+            lambda: P.prox_fp8_quantize(meta(1, many - 2), meta(1, many - 2, dtype=f8), meta(1, many // 128, dtype=f32)),
+            lambda: P.prox_expert_combine(meta(8, 16), meta(many, 2, dtype=i32), meta(many, 2, dtype=f32), meta(many, 16)),
+            lambda: P.prox_expert_combine(meta(8, 16), meta(1, many, dtype=i32), meta(1, many, dtype=f32), meta(1, 16)),
+            lambda: P.prox_expert_combine(meta(many, 16), meta(1, 2, dtype=i32), meta(1, 2, dtype=f32), meta(1, 16)),
+            lambda: P.prox_expert_route(meta(many, 8), *(meta(many, 2, dtype=d) for d in (i32, f32)),
+                                        meta(9, dtype=i32), meta(2 * many, dtype=i32), meta(many, 2, dtype=i32),
+                                        meta(256, dtype=torch.uint8)),
+            lambda: P.prox_expert_route(meta(1, many), *(meta(1, 2, dtype=d) for d in (i32, f32)),
+                                        meta(many + 1, dtype=i32), meta(2, dtype=i32), meta(1, 2, dtype=i32),
+                                        meta(256, dtype=torch.uint8)),
+            lambda: P.prox_moe_ffn(_layer(), meta(many, 64), meta(many, 64, dtype=f32), meta(256, dtype=torch.uint8))):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
