@@ -19,6 +19,18 @@ def test_oracle_holds_quotients_at_the_largest_code():
     assert q[0, :4].tolist() == [448, -448, 208, 1]
 
 
+def test_oracle_cuts_products_by_hand():
+    """Steps of 2^(e - 13) for the largest sum e of exponents in the eight."""
+    a, w = np.zeros((1, 16)), np.zeros((1, 16))
+    a[0, :3], w[0, :3] = [256, 2.0 ** -6, -2.0 ** -6], [256, 1.5, 1.5]  # e 16: multiples of 8
+    a[0, 8:10], w[0, 8:10] = [2.0 ** -6, 3.0], [1.5, 0.5]               # the next eight: e 0
+    assert O.cut_product(a, w)[0, 0] == 65536 + 1.5 * 2.0 ** -6 + 1.5
+    a[0, 0], w[0, 0] = 2.0 ** -9, 256                                   # subnormal: e 2 although the product is 0.5
+    a[0, 1], w[0, 1] = 13 * 2.0 ** -9, 9 * 2.0 ** -9                    # 117 2^-18: multiples of 2^-11
+    a[0, 2:], w[0, 2:] = 0, 0
+    assert O.cut_product(a, w)[0, 0] == 0.5
+
+
 # ------------------------------------------------- sizes that do not fit 32 bits
 WIDE = 1 << 32  # a size of WIDE + 2 would reach the library as 2
 

@@ -38,6 +38,32 @@ def test_quantize_where_the_scale_is_a_few_subnormal_steps(block_rows):
     assert abs(rq).max() == 448
 
 
+# ---------------------------------------------------------------- products
+def codes(g, shape, subnormal):
+    """Random e4m3 codes, none of them NaN; subnormal: that share of them 0 to 7."""
+    c = g.integers(0, 256, shape)
+    c = np.where(g.random(shape) < subnormal, c & 0x87, c)
+    c = np.where((c & 0x7F) == 0x7F, 0, c).astype(np.uint8)
+    return torch.from_numpy(c).cuda().view(FP8)
+
+
+@pytest.mark.parametrize("subnormal", [0.0, 0.5, 0.9])
+@pytest.mark.parametrize("rows,n,k", [(5, 40, 144), (130, 600, 128), (70, 130, 1040)])
+def test_e4m3_products_are_cut_as_stated(rows, n, k, subnormal):
+    """fp32 results of e4m3 products against the rule by which the matrix cores cut
+    small products: what is left is added in fp32, (K + 8) 2 EPS of the magnitudes.
+    Codes over the whole range: where the cut counts most, it is a thousand times
+    that.  Scales of one."""
+    g = np.random.default_rng(rows + n)
+    a, w = codes(g, (rows, k), subnormal), codes(g, (1, n, k), subnormal)
+    e = P.ProxExperts(w, scale=torch.ones(1, -(-n // 128), -(-k // 128), device="cuda"))
+    out = torch.empty(rows, n, device="cuda")
+    P.prox_grouped_matmul(e, a, out, a_scale=torch.ones(rows, -(-k // 128), device="cuda"))
+    ha, hw = (t.float().cpu().numpy().astype(np.float64) for t in (a, w[0]))
+    off = np.abs(out.cpu().numpy() - O.cut_product(ha, hw))
+    assert (off <= (k + 8) * 2 * 2.0 ** -24 * (np.abs(ha) @ np.abs(hw).T)).all()
+
+
 # ------------------------------------------------------------------ router
 @pytest.mark.parametrize("e", [5, 64, 65, 128])
 def test_route_in_one_launch_is_one_block(e):
