@@ -163,9 +163,9 @@ def test_product_inner_sizes(k, dtype):
         p.check(f"k {k} rows {rows}")
 
 
-# (rows of the groups, outputs): together with k and gating these take every tile
-# shape that the products choose among (from 32 x 32 in four groups of waves to
-# 256 x 256, whose last tiles have more or less than half their tokens)
+# (rows of the groups, outputs): together with k and gating these take tiles from
+# 32 x 32 in four groups of waves to 256 x 256, whose last ones have more or less than
+# half their tokens (test_gpu_experts_kernels.py runs every kernel)
 LARGE = [([700, 3, 0, 900], 1045), ([2100, 0, 129, 128, 1, 700], 2052), ([4000], 2306), ([600, 0, 140], 4101)]
 
 

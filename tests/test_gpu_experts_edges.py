@@ -81,3 +81,52 @@ def test_route_in_one_launch_is_one_block(e):
             assert "route_small_kernel" in found[0][0], found
         else:
             assert [f[1] for f in found] == [3, 3], (t, found)
+
+
+# ------------------------------------------------------------ run together
+@pytest.mark.parametrize("act", [P.PROX_ACT_SILU, P.PROX_ACT_GELU_TANH])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+def test_moe_ffn_equals_its_operators_on_a_prompt(dtype, act):
+    """Enough rows for the products' large tiles: the layer call gives the bits of the
+    single calls, each of which is tested against fp64.  A token without a finite
+    logit has none; the workspace holds NaN before the call."""
+    E, d, f, k, t = 5, 1056, 2064, 3, 900
+    base = torch.float32 if dtype == "f32" else torch.bfloat16
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    x, router, up, gate, down = (torch.randn(s, device="cuda", generator=gen) for s in
+                                 ((t, d), (E, d), (E, f, d), (E, f, d), (E, d, f)))
+    x, router, up, gate, down = (v.to(base) for v in (x, router * 0.1, up / 32, gate / 32, down / 45))
+    x[5, 0] = -float("inf")
+    router[:, 0] = 0.25  # every logit of token 5 is -inf
+    if dtype == "fp8":
+        def e4m3(w, block_rows=1):
+            q = torch.empty(w.shape, device="cuda", dtype=FP8)
+            s = torch.empty(-(-w.shape[0] // block_rows), -(-w.shape[1] // 128), device="cuda")
+            P.prox_fp8_quantize(w, q, s, block_rows=block_rows)
+            return q, s
+        (up, us), (gate, gs), (down, ds) = (map(torch.stack, zip(*(e4m3(w, 128) for w in m))) for m in (up, gate, down))
+        experts = P.ProxExperts(up, gate, scale=us, gate_scale=gs, activation=act), P.ProxExperts(down, scale=ds)
+    else:
+        experts = P.ProxExperts(up, gate, activation=act), P.ProxExperts(down)
+    layer = P.ProxMoeLayer(router, *experts, k)
+    y = torch.empty(t, d, device="cuda")
+    ws = torch.full((P.prox_moe_workspace_size(layer, t),), 255, dtype=torch.uint8, device="cuda")
+    P.prox_moe_ffn(layer, x, y, ws)
+
+    logits = torch.empty(t, E, device="cuda")
+    P.prox_grouped_matmul(P.ProxExperts(router[None]), x, logits)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    idx, off, rt, ro = (torch.empty(s, **i32) for s in ((t, k), (E + 1,), (t * k,), (t, k)))
+    w = torch.empty(t, k, device="cuda")
+    P.prox_expert_route(logits, idx, w, off, rt, ro,
+                        torch.empty(P.prox_expert_route_workspace_size(t, E, k), dtype=torch.uint8, device="cuda"))
+    assert (idx[5] == -1).all() and int(off[-1]) == (t - 1) * k
+    h, o = (torch.zeros(t * k, n, device="cuda", dtype=base) for n in (f, d))
+    a, xs = e4m3(x) if dtype == "fp8" else (x, None)
+    P.prox_grouped_matmul(layer.up, a, h, offsets=off, row_index=rt, a_scale=xs)
+    hin, hs = e4m3(h) if dtype == "fp8" else (h, None)
+    P.prox_grouped_matmul(layer.down, hin, o, offsets=off, a_scale=hs)
+    y2 = torch.empty(t, d, device="cuda")
+    P.prox_expert_combine(o, ro, w, y2)
+    assert torch.equal(y, y2) and torch.isfinite(y).all() and (y[5] == 0).all() and (y[:5] != 0).any()
