@@ -599,8 +599,7 @@ int route_blocks(int tokens) {
 
 }  // namespace
 
-size_t route_workspace(int tokens, int experts, int top_k) {
-  (void)top_k;
+size_t route_workspace(int tokens, int experts) {
   return (static_cast<size_t>(route_blocks(tokens)) * experts * sizeof(int) + 255) & ~static_cast<size_t>(255);
 }
 

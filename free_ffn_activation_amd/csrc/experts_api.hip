@@ -120,7 +120,7 @@ MoePlan moe_plan(const prox_moe_layer* L, int tokens) {
   p.offsets = part((static_cast<size_t>(L->up.n_groups) + 1) * 4);
   p.row_token = part(rows * 4);
   p.row_of = part(rows * 4);
-  p.route = part(route_workspace(tokens, L->up.n_groups, L->top_k));
+  p.route = part(route_workspace(tokens, L->up.n_groups));
   p.h = part(rows * f * es);
   p.o = part(rows * d * es);
   p.xq = part(fp8 ? t * d : 0);
@@ -204,7 +204,7 @@ PROX_API prox_status prox_expert_route_workspace_size(int32_t n_tokens, int32_t 
     if (!bytes) return fail(PROX_ERR_INVALID_ARG, "bytes is NULL");
     const prox_status st = check_route_shape(n_tokens, n_experts, top_k);
     if (st != PROX_OK) return st;
-    *bytes = route_workspace(n_tokens, n_experts, top_k);
+    *bytes = route_workspace(n_tokens, n_experts);
     return PROX_OK;
   } catch (...) {
     return fail(PROX_ERR_INTERNAL, "unexpected exception");
@@ -227,7 +227,7 @@ PROX_API prox_status prox_expert_route(const void* logits, int32_t logits_dtype,
     if (!aligned(logits, elem(logits_dtype)) || !aligned(expert_idx, 4) || !aligned(weight, 4) ||
         !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(row_of, 4) || !aligned(ws, 256))
       return fail(PROX_ERR_INVALID_ARG, "logits and outputs must be aligned by their elements, ws by 256 bytes");
-    const size_t need = route_workspace(n_tokens, n_experts, top_k);
+    const size_t need = route_workspace(n_tokens, n_experts);
     if (ws_bytes < need)
       return fail(PROX_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes, need);
     RouteArgs r;

@@ -45,7 +45,7 @@ struct RouteArgs {
   int* row_of;         // [tokens][top_k]
   int* block_count;    // workspace: rows of each expert by block, int32 or bytes
 };
-size_t route_workspace(int tokens, int experts, int top_k);
+size_t route_workspace(int tokens, int experts);  // bytes
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 
 struct QuantizeArgs {

@@ -70,9 +70,6 @@ __device__ __forceinline__ f32x4_t mma<Fp8Tag>(const Frag& w, const Frag& x, f32
                                                           __builtin_bit_cast(i32x8_t, x), acc, 0, 0, 0, 0, 0, 0);
 }
 
-// Sixteen zero bytes: the source of rows and chunks that do not exist.
-__device__ const u32x4_t g_zero16 = {0, 0, 0, 0};
-
 typedef __attribute__((address_space(3))) uint8_t* lds_ptr_t;
 __device__ __forceinline__ uint32_t lds_offset(void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr_t)(p)));
