@@ -32,7 +32,7 @@ FLAGS = [
     "-fvisibility=hidden", "-munsafe-fp-atomics",
     # packed fp32 VALU ops are kept out of every kernel on this target
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-Wno-unused-command-line-argument", "-Wno-inline-asm",
+    "-Wno-unused-command-line-argument",
 ]
 
 # Host-only instrumentation: every sanitizer flag is routed to the host

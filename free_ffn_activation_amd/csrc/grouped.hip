@@ -75,6 +75,10 @@ __device__ __forceinline__ uint32_t lds_offset(void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr_t)(p)));
 }
 
+// A copy's LDS address is in m0, a reserved register: the compiler says so at every
+// copy, and uses m0 nowhere else in these kernels.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 // 16 bytes per lane from memory to LDS at byte `to` + 16 * lane (`to` is
 // uniform).  Written out, since behind the builtin the compiler waits for every
 // copy under way before it reads any LDS; the copies have no result register,
@@ -92,6 +96,7 @@ __device__ __forceinline__ void copy16(const uint8_t* base, uint32_t offset, uin
 __device__ __forceinline__ void copy4(const void* src, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(src) : "m0");
 }
+#pragma clang diagnostic pop
 
 struct Item {
   int group, row0, rows, channel_tile;  // rows: those of the tile, 1 .. BT
