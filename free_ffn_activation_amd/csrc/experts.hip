@@ -75,11 +75,12 @@ __host__ __device__ inline int route_tokens_per_block(int tokens) {
 // holds the experts l + kLanes i, i < kPer, and its slots l and l + kLanes.  Each round
 // takes the token's largest key, then the lowest expert that has it, by token_all.  A
 // round is a chain of dependent instructions, so what bounds a launch is their number
-// per token (the logits of 8191 x 128 are read in 0.6 us, the launch takes 6): several
-// tokens share one instruction (with the same second launch, us: 65536 tokens of 128
-// experts 39.6, a wave per token 73; 8191 of 512 23 and 56).  A whole wave finds the
-// lowest expert by ballots, which are shorter than its second reduction (1024 experts:
-// 77 and 82).  id: the experts of this lane's slots, or -1.
+// per token (the logits of 8191 x 128 are read in 0.6 us, the launch takes 6; 65536 x
+// 128 in fp32: 13,700 vector instructions a SIMD, of four cycles each, are some 26 of
+// its 31 us): several tokens share one instruction (with the same second launch, us:
+// 65536 tokens of 128 experts 39.6, a wave per token 73; 8191 of 512 23 and 56).  A whole
+// wave finds the lowest expert by ballots, which are shorter than its second reduction
+// (1024 experts: 77 and 82).  id: the experts of this lane's slots, or -1.
 template <int kPer, int kLanes>
 __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int end, int lane, int (&id)[2]) {
   constexpr int kSlots = kLanes < kMaxTopK ? 2 : 1;
@@ -575,6 +576,8 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineArgs a, int blocks_
   }
 }
 
+// kVec 8 needs whole vectors in aligned rows; other n, strides and addresses take
+// kVec 1, each element a load of its own.
 template <typename T, int kOut, int kVec>
 hipError_t launch_combine_typed(const CombineArgs& a, hipStream_t s) {
   const int threads = std::min(256, ((a.n + kVec - 1) / kVec + 63) / 64 * 64);

@@ -739,13 +739,14 @@ hipError_t launch_tile(const GroupedArgs& a, hipStream_t s) {
 //   rounds * max(latency, blocks / CUs * cost),
 // is taken.  What the host knows is rows, groups and sizes, not how the rows
 // spread: a group of m rows on average counts as m / tokens + 1/2 tiles.  The
-// figures (us a step) are those that choose best on MI355X over 920 products of 1
-// to 64 groups, 1 to 1024 rows a group, n 256 to 12288 and k 256 to 12288: 3 % from
-// the best of all shapes in the mean for 16- and 8-bit types, 8 % for fp32 (by
-// thresholds on m and on the number of blocks: 6 and 12 %).  For example (bf16,
-// us): 64 groups, n 2048, k 1024, m 256: wide 114, 64 x 128 tiles 140; m 16: 64 x 128
-// 53, wide 60; one group, n = k = 4096, m 128: 32 x 64 in one K group 20, 32 x 32 in
-// four 15.
+// figures (us a step) were fitted on MI355X over 920 products of 1 to 64 groups, 1
+// to 1024 rows a group, n 256 to 12288 and k 256 to 12288.  With the present stores,
+// over 888 such products, the choice is 1.6 % (bf16), 1.4 % (fp8) and 1.8 % (fp32)
+// behind the best of these shapes in the mean, 5 % at the ninetieth hundredth, and
+// 33, 37 and 43 % at worst (fp32: 16 groups of 65 rows, n 1500, k 1008: 64 x 128 74.5
+// us, 32 x 32 in two K groups 52).  For example (bf16, us): 64 groups, n 2048, k 1024,
+// m 256: wide 115, 64 x 128 tiles 143; m 16: 32 x 64 55, wide 61; one group, n = k =
+// 4096, m 128: 32 x 32 in two K groups 17, 32 x 64 in one 19.
 enum Shape { kWide, k128x256, k64x128, k64x64, k32x64, k32x32by2, k32x32by4, kShapes };
 struct ShapeTime {
   int tokens, channels, groups;  // a block's tile, and how many groups of waves share k
@@ -754,8 +755,10 @@ struct ShapeTime {
 constexpr ShapeTime kTimes[kShapes] = {
     {256, 256, 1, 2.0f, 2.4f},  {128, 256, 1, 1.2f, 1.6f},  {64, 128, 1, 0.45f, 0.51f}, {64, 64, 1, 0.30f, 0.29f},
     {32, 64, 1, 0.26f, 0.23f},  {32, 32, 2, 0.25f, 0.25f},  {32, 32, 4, 0.43f, 0.71f}};
-// fp32 products are bound by the matrix cores (256 flops per clock and CU) even in
-// small tiles; the two large shapes are not built for them
+// fp32 products run at 256 flops per clock and CU at most, which 64 x 128 tiles reach
+// to three quarters (16 groups of 1024 rows, n = k = 1024: matrix cores 72 % busy, 307
+// us, 112 TFLOP/s; one group of 4096 rows, n = k = 2048: 126 of the 153 of a large
+// library product); the two large shapes are not built for them
 constexpr ShapeTime kTimesF32[kShapes] = {
     {0, 0, 0, 0, 0},            {0, 0, 0, 0, 0},            {64, 128, 1, 1.12f, 1.35f}, {64, 64, 1, 0.61f, 0.72f},
     {32, 64, 1, 0.61f, 0.50f},  {32, 32, 2, 0.47f, 0.43f},  {32, 32, 4, 0.68f, 0.89f}};

@@ -486,7 +486,9 @@ typedef struct {
  * a_scale    PROX_FP8: device fp32 [a_rows][ceil(k/128)], the scale of each 128
  *            inputs of a row (prox_fp8_quantize, block_rows 1); else ignored
  * row_index  device [rows] int32: src(r) = row_index[r]; an index outside
- *            [0, a_rows) gives a row of zeros in out.  NULL: src(r) = r
+ *            [0, a_rows) gives a row of zeros in out.  NULL: src(r) = r.  a_rows is
+ *            at least 1 where rows is (PROX_ERR_INVALID_ARG), and without a
+ *            row_index at least rows
  * offsets    device [n_groups + 1] int32, ascending, offsets[0] >= 0 and
  *            offsets[n_groups] <= rows (values outside [0, rows] are clamped).
  *            Groups may be empty.  NULL: one group of all rows (n_groups 1)
@@ -499,7 +501,9 @@ typedef struct {
  * product of two codes is cut off, towards zero, to a multiple of 2^(e - 13), e the
  * largest sum of two codes' exponents (a subnormal code counts as -6); the eights
  * and the blocks of 128 are added in fp32, whatever the type of out.  With fp32
- * results that is about 3e-5 of the result's norm for usual activations.
+ * results that is about 3e-5 of the result's norm for usual activations.  The two
+ * scales of a block are multiplied first, in fp32, so their product must be finite,
+ * and is exact to 2^-24 relative or 2^-150 absolute.
  * The offsets are read on the device: no host synchronisation, and a captured
  * call may be replayed with other offsets and row indices.  No workspace.
  * Asynchronous.
@@ -564,7 +568,9 @@ prox_status prox_fp8_quantize(const void* x, int32_t x_dtype, int32_t rows, int3
  *   weight  device [n_tokens][top_k] fp32
  *   y       device [n_tokens][n] of y_dtype (PROX_F32 or PROX_BF16, overwritten),
  *           rows y_stride elements apart
- * 1 <= top_k <= 32, n <= 2^24, n_tokens * top_k <= 2^30.  Asynchronous.
+ * 1 <= top_k <= 32, n <= 2^24, n_tokens * top_k <= 2^30.  Any n and strides: eight
+ * values at a time where n is a multiple of 8 and h, y and their rows are 16-byte
+ * aligned, else one by one (a prompt takes 2.8 times as long).  Asynchronous.
  */
 prox_status prox_expert_combine(const void* h, int32_t h_dtype, int32_t h_rows, int64_t h_stride,
                                 const int32_t* row_of, const float* weight, int32_t n_tokens, int32_t top_k, int32_t n,

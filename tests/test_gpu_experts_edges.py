@@ -64,6 +64,18 @@ def test_e4m3_products_are_cut_as_stated(rows, n, k, subnormal):
     assert (off <= (k + 8) * 2 * 2.0 ** -24 * (np.abs(ha) @ np.abs(hw).T)).all()
 
 
+@pytest.mark.parametrize("rows", [3, 300])
+def test_e4m3_scales_are_multiplied_in_fp32(rows):
+    """Two scales whose product is subnormal, 2^-148: it is exact, and so is the
+    result; products of scales that are too small for fp32 count as zero."""
+    a, w = torch.ones(rows, 128, device="cuda").to(FP8), torch.ones(1, 500, 128, device="cuda").to(FP8)
+    out = torch.empty(rows, 500, device="cuda")
+    for x, want in ((2.0 ** -74, 2.0 ** -141), (2.0 ** -80, 0.0)):
+        e = P.ProxExperts(w, scale=torch.full((1, 4, 1), x, device="cuda"))
+        P.prox_grouped_matmul(e, a, out, a_scale=torch.full((rows, 1), x, device="cuda"))
+        assert (out.double() == want).all()
+
+
 # ------------------------------------------------------------------ router
 @pytest.mark.parametrize("e", [5, 64, 65, 128])
 def test_route_in_one_launch_is_one_block(e):
