@@ -42,7 +42,8 @@ HOSTSAN_FLAGS = [
     "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer",
     "-shared-libsan", "-g",
 ]
-HOSTSAN_TESTS = ["tests/test_abi_cpu.py", "tests/test_budget_cpu.py", "tests/test_experts_cpu.py"]
+HOSTSAN_TESTS = ["tests/test_abi_cpu.py", "tests/test_budget_cpu.py", "tests/test_experts_cpu.py",
+                 "tests/test_experts_edges_cpu.py"]
 
 
 def hipcc() -> str:

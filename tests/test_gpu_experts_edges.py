@@ -64,6 +64,29 @@ def test_e4m3_products_are_cut_as_stated(rows, n, k, subnormal):
     assert (off <= (k + 8) * 2 * 2.0 ** -24 * (np.abs(ha) @ np.abs(hw).T)).all()
 
 
+@pytest.mark.parametrize("groups", [127, 256, 257, 600, 1023, 1024])
+@pytest.mark.parametrize("most,n", [(2, 40), (40, 300), (700, 520)])
+def test_product_of_many_groups(groups, most, n):
+    """More groups than a block has threads: each thread then looks through several.
+    Up to `most` rows a group, two thirds of them without any."""
+    k = 64
+    g = np.random.default_rng(groups + most)
+    sizes = np.where(g.random(groups) < 2 / 3, 0, g.integers(0, most + 1, groups))
+    sizes[-1] = 1
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    rows = int(off[-1]) + 2
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(groups)
+    a, w = (torch.randn(s, device="cuda", generator=gen).to(torch.bfloat16) for s in ((rows, k), (groups, n, k)))
+    out = torch.full((rows, n), 7.0, device="cuda")
+    P.prox_grouped_matmul(P.ProxExperts(w), a, out, offsets=torch.from_numpy(off).cuda())
+    assert (out[-2:] == 7).all()
+    for j in np.flatnonzero(sizes):
+        x, m = a[off[j]:off[j + 1]].double(), w[j].double()
+        bad = (out[off[j]:off[j + 1]] - x @ m.T).abs() > (k + 8) * 2 * 2.0 ** -24 * (x.abs() @ m.abs().T)
+        assert not bad.any(), f"group {j}"
+
+
 @pytest.mark.parametrize("rows", [3, 300])
 def test_e4m3_scales_are_multiplied_in_fp32(rows):
     """Two scales whose product is subnormal, 2^-148: it is exact, and so is the
@@ -93,6 +116,20 @@ def test_route_in_one_launch_is_one_block(e):
             assert "route_small_kernel" in found[0][0], found
         else:
             assert [f[1] for f in found] == [3, 3], (t, found)
+
+
+# ----------------------------------------------------------------- combine
+@pytest.mark.parametrize("n", [64, 33])
+def test_combine_reads_nothing_of_slots_without_a_row(n):
+    """Weights of NaN in such slots, and rows of NaN that no slot names."""
+    h = torch.full((6, n), float("nan"), device="cuda")
+    h[2], h[4] = 3.0, 5.0
+    row_of = torch.tensor([[2, -1, 4], [-1, 6, -7], [2, 2, 1 << 30]], device="cuda", dtype=torch.int32)
+    nan = float("nan")
+    w = torch.tensor([[2.0, nan, 1.0], [nan, nan, nan], [1.0, 0.5, nan]], device="cuda")
+    y = torch.empty(3, n, device="cuda")
+    P.prox_expert_combine(h, row_of, w, y)
+    assert torch.equal(y, torch.tensor([[11.0], [0.0], [4.5]], device="cuda").expand(3, n))
 
 
 # ------------------------------------------------------------ run together
