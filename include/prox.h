@@ -545,7 +545,7 @@ prox_status prox_expert_route(const void* logits, int32_t logits_dtype, int32_t 
  *   scale = fp32(amax / 448), amax the block's largest |x|
  *   q     = e4m3(fp32(x / scale)), to nearest, ties to even, at most +-448
  *           (larger quotients arise where the scale is a few subnormal steps)
- * A block whose scale is 0 (all zeros, or values below 2^-141) has codes 0; a
+ * A block whose scale is 0 (amax at most 224 2^-149) has codes 0; a
  * block that holds an infinity or NaN has scale NaN and codes NaN.
  *   x           device [rows][k], PROX_F32 or PROX_BF16, rows x_stride elements
  *               apart; x and its rows 16-byte aligned, k a multiple of 16
